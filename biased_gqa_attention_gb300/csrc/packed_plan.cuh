@@ -1,0 +1,44 @@
+// packed_plan.cuh -- the work list of a packed prefill: which query tiles there
+// are, the dearest first.
+#pragma once
+
+#include "common.cuh"
+#include "paged.h"
+#include "ptx.cuh"
+
+namespace extkv {
+
+// One tile of queries: tokens tok0 .. of the sequence whose first row is
+// `row0` and which has `len` tokens.
+struct PackedItem {
+  int row0, len, tok0, pad;
+};
+
+struct PackedParams {
+  void* y;
+  const void* q;
+  const void* k;
+  const void* v;
+  const int64_t* cu;
+  float c;  // scale * log2(e)
+  int causal, window, T, B, Hq, Hkv, g, D;
+  int64_t q_stride, k_stride, v_stride;
+  int pk;        // query heads of one KV head in a tile (a power of two that divides g)
+  int tile_tok;  // tokens of a tile
+  int heads;     // head groups: Hq / pk
+  int max_items;
+  int* count;         // items, written by the plan kernel
+  PackedItem* items;
+  int32_t* status;
+  uint32_t wait_limit;
+};
+
+// The keys some row of the tile attends, [lo, hi).
+__device__ __forceinline__ int2 item_keys(const PackedParams& p, int len, int tok0) {
+  const int last = min(len, tok0 + p.tile_tok);
+  return make_int2(p.window > 0 ? max(0, tok0 - p.window + 1) : 0, p.causal ? last : len);
+}
+
+constexpr int kPlanThreads = 1024;
+
+}  // namespace extkv

@@ -1,0 +1,261 @@
+// packed_prefill.cu -- attention over prompts packed one after another: the
+// plan kernel (the list of query tiles), the fp32 SIMT kernel and the choice
+// between it and the tensor-core kernel.
+#include <algorithm>
+
+#include "internal.h"
+#include "packed_plan.cuh"
+#include "simt_tile.cuh"
+#include "tma_host.h"
+
+namespace extkv {
+
+namespace {
+
+// One CTA.  A causal prompt's tiles cost from one to len / 128 key tiles, so the
+// list is sorted by cost, dearest first (a counting sort over 1024 cost
+// classes): CTAs that take items in turn then end together.  The order within a
+// class follows the atomics; every item is computed alone, so no result
+// depends on it.  Also checks cu_seqlens: a bad one leaves an empty list.
+__global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedParams p) {
+  __shared__ int hist[1024];
+  __shared__ int warp_sum[32];
+  __shared__ int bad;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  hist[tid] = 0;
+  if (tid == 0) bad = 0;
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
+  __syncthreads();
+  bool mine_bad = false;
+  for (int b = tid; b <= p.B; b += kPlanThreads) {
+    const int64_t x = p.cu[b];
+    mine_bad |= x < 0 || x > p.T || (b > 0 && p.cu[b - 1] > x);
+  }
+  if (mine_bad) bad = 1;
+  __syncthreads();
+  if (bad) {
+    if (tid == 0) {
+      report(p.status, EXTKV_DEV_BAD_SEQLENS);
+      *p.count = 0;
+    }
+    return;
+  }
+  const int most = p.T / 128 + 2;  // an item's cost is below this
+  auto cls = [&](int len, int tok0) {
+    const int2 k = item_keys(p, len, tok0);
+    const int cost = (k.y + 127) / 128 - k.x / 128;
+    return 1023 - static_cast<int>(static_cast<int64_t>(cost) * 1023 / most);
+  };
+  // a warp per sequence, a lane per tile
+  for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+    const int len = static_cast<int>(p.cu[b + 1] - p.cu[b]);
+    for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok)
+      atomicAdd(&hist[cls(len, static_cast<int>(t))], 1);
+  }
+  __syncthreads();
+  const int n = hist[tid];
+  int inc = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int x = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += x;
+  }
+  if (lane == 31) warp_sum[warp] = inc;
+  __syncthreads();
+  int off = 0;
+  for (int w = 0; w < warp; ++w) off += warp_sum[w];
+  __syncthreads();
+  hist[tid] = off + inc - n;
+  if (tid == kPlanThreads - 1) *p.count = min(off + inc, p.max_items);
+  __syncthreads();
+  for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+    const int row0 = static_cast<int>(p.cu[b]), len = static_cast<int>(p.cu[b + 1]) - row0;
+    for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok) {
+      const int at = atomicAdd(&hist[cls(len, static_cast<int>(t))], 1);
+      if (at < p.max_items && EXTKV_IN(at, 1, p.max_items, p.status))
+        p.items[at] = PackedItem{row0, len, static_cast<int>(t), 0};
+    }
+  }
+}
+
+// ---- SIMT (fp32, other head sizes) ---------------------------------------------------
+// A CTA takes a tile of 32 query rows (tokens by heads of one KV head), eight a
+// warp, and streams the keys through two shared-memory stages that its four
+// warps share.
+
+constexpr int kWarps = 4;
+constexpr int kTileRows = kWarps * kRows;
+
+__device__ __forceinline__ void cp_async_16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+template <typename T>
+__host__ __device__ constexpr int simt_stride(int D) {
+  return D + 16 / static_cast<int>(sizeof(T));  // rows start in different banks
+}
+
+template <typename T, int DPL, int KT>
+__global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const PackedParams p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, D = p.D;
+  ptx::grid_dependency_wait();
+  ptx::grid_launch_dependents();
+  const int stride = simt_stride<T>(D), stage = 2 * KT * stride;
+  T* ring = reinterpret_cast<T*>(smem);
+  float* qs = reinterpret_cast<float*>(smem + 2 * stage * sizeof(T)) + warp * (kRows * D + kRows * KT);
+  float* ps = qs + kRows * D;
+  const int chunks = D * static_cast<int>(sizeof(T)) / 16;
+  const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
+  SimtState<DPL> st;
+  for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
+    const int64_t at = w / p.heads;
+    if (!EXTKV_IN(at, 1, p.max_items, p.status)) break;
+    const PackedItem item = p.items[at];
+    const int h0 = static_cast<int>(w - at * p.heads) * p.pk, hk = h0 / p.g;
+    const int2 keys = item_keys(p, item.len, item.tok0);
+    st.clear();
+    for (int i = lane; i < kRows * D; i += 32) {
+      const int r = i / D, d = i - r * D, row = warp * kRows + r;
+      const int tok = item.tok0 + row / p.pk;
+      qs[i] = tok < item.len ? Elem<T>::load(static_cast<const T*>(p.q) + (item.row0 + tok) * p.q_stride +
+                                                 static_cast<int64_t>(h0 + row % p.pk) * D,
+                                             d) * p.c
+                             : 0.f;
+    }
+    auto load = [&](int t, int s) {
+      const int k0 = keys.x + t * KT;
+      const uint32_t kd = ptx::smem_u32(ring + s * stage), vd = kd + KT * stride * sizeof(T);
+      for (int x = tid; x < KT * chunks; x += kWarps * 32) {
+        const int r = x / chunks, ch = x - r * chunks;
+        const bool in = k0 + r < keys.y;  // keys past the range are filled with zeros
+        const int64_t row = in ? item.row0 + k0 + r : 0;
+        const uint32_t to = r * stride * sizeof(T) + ch * 16;
+        cp_async_16(kd + to, reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.k) + row * p.k_stride + hk * D) + ch * 16,
+                    in ? 16 : 0);
+        cp_async_16(vd + to, reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.v) + row * p.v_stride + hk * D) + ch * 16,
+                    in ? 16 : 0);
+      }
+    };
+    const int nt = (keys.y - keys.x + KT - 1) / KT;
+    load(0, 0);
+    cp_async_commit();
+    for (int t = 0; t < nt; ++t) {
+      if (t + 1 < nt) load(t + 1, (t + 1) & 1);
+      cp_async_commit();
+      cp_async_wait<1>();
+      __syncthreads();
+      const int k0 = keys.x + t * KT;
+      int lo[kRows], hi[kRows];
+      bool any = false;
+#pragma unroll
+      for (int r = 0; r < kRows; ++r) {
+        const int tok = item.tok0 + (warp * kRows + r) / p.pk;
+        int a = p.window > 0 ? max(0, tok - p.window + 1) : 0, b = p.causal ? tok + 1 : item.len;
+        if (tok >= item.len) a = b = 0;
+        lo[r] = min(max(a - k0, 0), KT);
+        hi[r] = min(max(b - k0, 0), KT);
+        any |= lo[r] < hi[r];
+      }
+      const T* kt = ring + (t & 1) * stage;
+      if (any) simt_tile<T, DPL, KT>(st, kt, kt + KT * stride, stride, qs, ps, D, lo, hi, kRows);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int r = 0; r < kRows; ++r) {
+      const int row = warp * kRows + r, tok = item.tok0 + row / p.pk;
+      if (tok < item.len) {
+        const float inv = st.l[r] != 0.f ? 1.f / st.l[r] : 0.f;
+        const int64_t y0 = (static_cast<int64_t>(item.row0 + tok) * p.Hq + h0 + row % p.pk) * D;
+        T* y = static_cast<T*>(p.y);
+        if (EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status)) {
+#pragma unroll
+          for (int i = 0; i < DPL; ++i) {
+            const int d = lane + 32 * i;
+            if (d < D) y[y0 + d] = Elem<T>::from_float(st.acc[r][i] * inv);
+          }
+        }
+      }
+    }
+    __syncthreads();
+  }
+}
+
+template <typename T, int DPL, int KT>
+cudaError_t launch_simt(const PackedParams& p, cudaStream_t s) {
+  const size_t smem = 2 * 2 * KT * simt_stride<T>(p.D) * sizeof(T) +
+                      static_cast<size_t>(kWarps) * (kRows * p.D + kRows * KT) * 4;
+  auto k = packed_simt_kernel<T, DPL, KT>;
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), smem); e != cudaSuccess) return e;
+  const int64_t blocks = std::min<int64_t>(static_cast<int64_t>(p.max_items) * p.heads, int64_t(num_sms()) * 2);
+  PdlLaunch l(dim3(static_cast<unsigned>(blocks)), kWarps * 32, smem, s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <typename T>
+cudaError_t launch_simt_d(const PackedParams& p, cudaStream_t s) {
+  if (p.D <= 64) return launch_simt<T, 2, 32>(p, s);
+  if (p.D <= 128) return launch_simt<T, 4, 32>(p, s);
+  if (p.D <= 256) return launch_simt<T, 8, 16>(p, s);
+  return launch_simt<T, 16, 8>(p, s);
+}
+
+// The largest power of two that divides g, at most `cap`.
+int pack_heads(int64_t g, int cap) {
+  int pk = 1;
+  while (pk < cap && g % (2 * pk) == 0) pk *= 2;
+  return pk;
+}
+
+}  // namespace
+
+size_t packed_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
+  const int pk = pack_heads(Hq / Hkv, kTileRows);
+  const int64_t items = T * pk / kTileRows + B + 1;
+  return 256 + ((items * sizeof(PackedItem) + 255) & ~size_t(255));
+}
+
+cudaError_t launch_packed(const PackedArgs& a, const char** name) {
+  PackedParams p{};
+  p.y = a.y;
+  p.q = a.q;
+  p.k = a.k;
+  p.v = a.v;
+  p.cu = a.cu_seqlens;
+  p.c = a.scale * kLog2e;
+  p.causal = a.causal != 0;
+  p.window = a.window > 0 ? a.window : 0;
+  p.T = static_cast<int>(a.T);
+  p.B = static_cast<int>(a.B);
+  p.Hq = static_cast<int>(a.Hq);
+  p.Hkv = static_cast<int>(a.Hkv);
+  p.g = p.Hq / p.Hkv;
+  p.D = static_cast<int>(a.D);
+  p.q_stride = a.q_stride;
+  p.k_stride = a.k_stride;
+  p.v_stride = a.v_stride;
+  p.pk = pack_heads(p.g, kTileRows);
+  p.tile_tok = kTileRows / p.pk;
+  p.heads = p.Hq / p.pk;
+  p.max_items = static_cast<int>(a.T / p.tile_tok + a.B + 1);
+  uint8_t* ws = static_cast<uint8_t*>(a.workspace);
+  p.count = reinterpret_cast<int*>(ws);
+  p.items = reinterpret_cast<PackedItem*>(ws + 256);
+  p.status = a.status;
+  PdlLaunch l(dim3(1), kPlanThreads, 0, a.stream);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, packed_plan_kernel, p);
+  if (e != cudaSuccess) return e;
+  *name = a.dtype == EXTKV_F32 ? "packed_simt_f32" : "packed_simt_bf16";
+  e = a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);
+  if (e == cudaSuccess) note_launches(2);
+  return e;
+}
+
+}  // namespace extkv

@@ -9,7 +9,7 @@ from __future__ import annotations
 import ctypes
 import os
 from dataclasses import dataclass
-from typing import Optional
+from typing import Optional, Sequence
 
 import torch
 
@@ -19,6 +19,7 @@ LIB_PATH = os.path.join(_HERE, "libextkv.so")
 EXTKV_F32, EXTKV_BF16 = 0, 1
 EXTKV_OK, EXTKV_ERR_INVALID_ARG, EXTKV_ERR_UNSUPPORTED, EXTKV_ERR_CUDA, EXTKV_ERR_DEVICE = 0, -1, -2, -3, -4
 EXTKV_DEV_BAD_WRITE_IDX, EXTKV_DEV_BAD_NONPAD, EXTKV_DEV_TIMEOUT, EXTKV_DEV_BOUNDS = 0x1, 0x2, 0x4, 0x8
+EXTKV_DEV_BAD_PAGE, EXTKV_DEV_BAD_SEQLENS = 0x10, 0x20
 ALGO_AUTO, ALGO_GENERIC, ALGO_DECODE, ALGO_PREFILL, ALGO_PREFILL_PAIR = 0, 1, 2, 3, 4
 ALGO_DECODE_STREAMK, ALGO_DECODE_CLUSTER = 5, 6
 
@@ -30,13 +31,21 @@ SYMBOLS = ("ext_kv_scatter", "build_static_cache_bias", "attention_ext_kv_worksp
            "extkv_last_error", "extkv_last_kernel", "extkv_last_launches", "extkv_set_algo",
            "extkv_set_wait_polls",
            "attention_ext_kv_noalloc",
-           "extkv_step_begin", "extkv_step_end", "extkv_step_launch", "extkv_step_free")
+           "extkv_step_begin", "extkv_step_end", "extkv_step_launch", "extkv_step_free",
+           "rotary_multi_axis", "paged_kv_append", "attention_paged_decode",
+           "attention_paged_decode_workspace_size", "attention_packed_prefill",
+           "attention_packed_prefill_workspace_size")
 
 
 class ExtKVError(RuntimeError):
     def __init__(self, code: int, message: str):
         super().__init__(f"extkv error {code}: {message}")
         self.code = code
+
+
+class _Rotary(ctypes.Structure):
+    _fields_ = [("n_axes", ctypes.c_int32), ("sections", ctypes.c_int32 * 4), ("rotary_dim", ctypes.c_int32),
+                ("interleaved", ctypes.c_int32), ("positions", ctypes.c_void_p), ("inv_freq", ctypes.c_void_p)]
 
 
 class _BiasSpec(ctypes.Structure):
@@ -93,6 +102,17 @@ def load(path: str = LIB_PATH):
     lib.extkv_step_launch.restype = I
     lib.extkv_step_free.argtypes = [P]
     lib.extkv_step_free.restype = None
+    I32, F, SZ, ROT = ctypes.c_int32, ctypes.c_float, ctypes.c_size_t, ctypes.POINTER(_Rotary)
+    lib.rotary_multi_axis.argtypes = [P, P, P, P, ROT, I64, I64, I64, I64, I64, I, P]
+    lib.paged_kv_append.argtypes = [P, P, P, P, P, P, P, P, P, ROT] + [I64] * 11 + [I, I32P, P]
+    lib.attention_paged_decode.argtypes = [P, P, P, P, P, P, F, I32] + [I64] * 8 + [I, P, SZ, I32P, P]
+    lib.attention_paged_decode_workspace_size.argtypes = [I64, I64, I64, I64, I]
+    lib.attention_paged_decode_workspace_size.restype = SZ
+    lib.attention_packed_prefill.argtypes = [P, P, P, P, P, F, I32, I32] + [I64] * 8 + [I, P, SZ, I32P, P]
+    lib.attention_packed_prefill_workspace_size.argtypes = [I64, I64, I64, I64, I64, I]
+    lib.attention_packed_prefill_workspace_size.restype = SZ
+    for name in ("rotary_multi_axis", "paged_kv_append", "attention_paged_decode", "attention_packed_prefill"):
+        getattr(lib, name).restype = I
     for name in ("ext_kv_scatter", "build_static_cache_bias", "attention_ext_kv", "attention_ext_kv_noalloc",
                  "extkv_clear_status", "extkv_read_status", "extkv_set_algo"):
         getattr(lib, name).restype = I
@@ -364,6 +384,294 @@ def attention_ext_kv_noalloc(y, q, k_cache, v_cache, nonpad, scale, bias=None,
                                            None if c is None else ctypes.byref(c), _p(nonpad),
                                            float(scale), B, Hq, Hkv, S_q, max_seq, D, _dt(q),
                                            _p(status), _stream(stream)))
+
+
+# ---- packed rows and a cache in pages ------------------------------------------------
+
+
+@dataclass
+class RotarySpec:
+    """extkv_rotary: rotary positions with one to four axes.  ``positions``
+    (axes, rows) int64 -- (axes, B, S) for rotary_multi_axis -- and ``inv_freq``
+    (rotary_dim/2,) float32 live on the device; pair i is turned by
+    positions[axis of i] * inv_freq[i], ``sections`` giving the pairs of each
+    axis in turn.  Pairs are elements (i, i + rotary_dim/2), or (2i, 2i+1) when
+    ``interleaved``."""
+    positions: torch.Tensor
+    inv_freq: torch.Tensor
+    sections: Sequence[int]
+    interleaved: bool = False
+
+    def _c(self, shape) -> _Rotary:
+        _need(self.inv_freq, "inv_freq", dims=1, dtype=torch.float32)
+        _need(self.positions, "positions", dtype=torch.int64)
+        n = len(self.sections)
+        if not 1 <= n <= 4:
+            raise ValueError("sections must name one to four axes")
+        if tuple(self.positions.shape) != (n, *shape):
+            raise ValueError(f"positions must be {(n, *shape)}, got {tuple(self.positions.shape)}")
+        if sum(self.sections) != self.inv_freq.shape[0]:
+            raise ValueError("sections must sum to the length of inv_freq (rotary_dim/2)")
+        return _Rotary(n, (ctypes.c_int32 * 4)(*[int(x) for x in self.sections]), 2 * self.inv_freq.shape[0],
+                       int(bool(self.interleaved)), _p(self.positions), _p(self.inv_freq))
+
+
+def _on_current_device(**tensors):
+    """Every tensor given is on the current CUDA device, where the call launches."""
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor, got {t.device}")
+        if t.device.index != torch.cuda.current_device():
+            raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
+def _need_rows(t, name, shape, dtype) -> int:
+    """(rows, H, D) with dense (H, D) rows; returns the elements between rows."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {tuple(shape)}, got {tuple(t.shape)}")
+    rows, H, D = shape
+    if t.numel() and ((D > 1 and t.stride(2) != 1) or (H > 1 and t.stride(1) != D)):
+        raise ValueError(f"the heads of {name} must be dense within a row")
+    return t.stride(0) if rows > 1 else H * D
+
+
+def _need_status(status):
+    _need(status, "status", dtype=torch.int32)
+    if status is not None and status.numel() < 4:
+        raise ValueError("status must hold 16 bytes")
+
+
+def _marshal_rotary(q_out, k_out, q, k, rotary: RotarySpec, stream):
+    first = q if q is not None else k
+    if first is None:
+        raise ValueError("q or k must be given")
+    for t, o, n in ((q, q_out, "q"), (k, k_out, "k")):
+        if (t is None) != (o is None):
+            raise ValueError(f"{n} and {n}_out must be given together")
+        _need(t, n, dims=4, dtype=first.dtype)
+        _need(o, n + "_out", dims=4, dtype=first.dtype)
+        if t is not None and (o.shape != t.shape or t.shape[0] != first.shape[0] or t.shape[2:] != first.shape[2:]):
+            raise ValueError("inconsistent q / k shapes")
+    B, _, S, D = first.shape
+    dt = _dt(first)
+    c = rotary._c((B, S))
+    _on_current_device(q=q, q_out=q_out, k=k, k_out=k_out, positions=rotary.positions, inv_freq=rotary.inv_freq)
+    return load().rotary_multi_axis, (_p(q_out), _p(k_out), _p(q), _p(k), ctypes.byref(c), B,
+                                      1 if q is None else q.shape[1], 1 if k is None else k.shape[1], S, D, dt,
+                                      _stream(stream)), (c, q_out, k_out, q, k, rotary)
+
+
+def rotary_multi_axis(q_out, k_out, q, k, rotary: RotarySpec, stream=None):
+    """Rotates q (B,Hq,S,D) into ``q_out`` and k (B,Hkv,S,D) into ``k_out`` by the
+    angles of ``rotary`` (positions (axes,B,S)); either pair may be None, and an
+    output may be its input."""
+    fn, args, _ = _marshal_rotary(q_out, k_out, q, k, rotary, stream)
+    _check(fn(*args))
+
+
+def prepare_rotary_multi_axis(q_out, k_out, q, k, rotary: RotarySpec, stream=None) -> PreparedCall:
+    """rotary_multi_axis with its arguments marshalled once (PreparedCall)."""
+    return PreparedCall(*_marshal_rotary(q_out, k_out, q, k, rotary, stream))
+
+
+def _need_pages(k_pages, v_pages, page_table, B, dtype):
+    for t, n in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        _need(t, n, dims=4, dtype=dtype)
+    if v_pages.shape != k_pages.shape:
+        raise ValueError("k_pages and v_pages must have one shape")
+    _need(page_table, "page_table", dims=2, dtype=torch.int64)
+    if page_table.shape[0] != B:
+        raise ValueError(f"page_table must have {B} rows, got {page_table.shape[0]}")
+
+
+def _marshal_append(k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens, rotary, q_out, q, status,
+                    stream):
+    dtype = k_pages.dtype
+    _need(write_idx, "write_idx", dims=1, dtype=torch.int64)
+    B = write_idx.shape[0]
+    _need_pages(k_pages, v_pages, page_table, B, dtype)
+    num_pages, Hkv, page_size, D = k_pages.shape
+    if k_new.dim() != 3:
+        raise ValueError(f"k_new must have 3 dims, got {tuple(k_new.shape)}")
+    T = k_new.shape[0]
+    ks = _need_rows(k_new, "k_new", (T, Hkv, D), dtype)
+    vs = _need_rows(v_new, "v_new", (T, Hkv, D), dtype)
+    _need(cu_seqlens, "cu_seqlens", dims=1, dtype=torch.int64)
+    if cu_seqlens is not None and cu_seqlens.shape[0] != B + 1:
+        raise ValueError(f"cu_seqlens must have {B + 1} entries, got {cu_seqlens.shape[0]}")
+    if cu_seqlens is None and T != B:
+        raise ValueError(f"without cu_seqlens there is one row per sequence: {T} rows for {B} sequences")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out must be given together")
+    qs, Hq = 0, 1
+    if q is not None:
+        if rotary is None:
+            raise ValueError("q is rotated; it needs rotary")
+        if q.dim() != 3:
+            raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+        Hq = q.shape[1]
+        qs = _need_rows(q, "q", (T, Hq, D), dtype)
+        _need(q_out, "q_out", dims=3, dtype=dtype)
+        if q_out.shape != q.shape:
+            raise ValueError("q_out must have q's shape")
+    _need_status(status)
+    dt = _dt(k_pages)
+    c = None if rotary is None else rotary._c((T,))
+    _on_current_device(k_pages=k_pages, v_pages=v_pages, k_new=k_new, v_new=v_new, page_table=page_table,
+                       write_idx=write_idx, cu_seqlens=cu_seqlens, q=q, q_out=q_out, status=status,
+                       positions=None if rotary is None else rotary.positions,
+                       inv_freq=None if rotary is None else rotary.inv_freq)
+    return load().paged_kv_append, (_p(k_pages), _p(v_pages), _p(k_new), _p(v_new), _p(page_table), _p(write_idx),
+                                    _p(cu_seqlens), _p(q_out), _p(q), None if c is None else ctypes.byref(c), T, B, Hq,
+                                    Hkv, D, num_pages, page_size, page_table.shape[1], qs, ks, vs, dt, _p(status),
+                                    _stream(stream)), \
+        (c, k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens, rotary, q_out, q, status)
+
+
+def paged_kv_append(k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens=None,
+                    rotary: Optional[RotarySpec] = None, q_out=None, q=None, status=None, stream=None):
+    """Writes packed rows k_new, v_new (T,Hkv,D) into the pages
+    (num_pages,Hkv,page_size,D) at slots write_idx[b].. of each sequence
+    (cu_seqlens None: one row per sequence).  With ``rotary`` (positions
+    (axes,T)) the K rows are rotated on the way, and q (T,Hq,D) into ``q_out``
+    when given.  k_new, v_new and q may have any row stride that is a multiple
+    of 16 bytes."""
+    fn, args, _ = _marshal_append(k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens, rotary, q_out, q,
+                                  status, stream)
+    _check(fn(*args))
+
+
+def prepare_paged_kv_append(k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens=None,
+                            rotary: Optional[RotarySpec] = None, q_out=None, q=None, status=None,
+                            stream=None) -> PreparedCall:
+    """paged_kv_append with its arguments marshalled once (PreparedCall)."""
+    return PreparedCall(*_marshal_append(k_pages, v_pages, k_new, v_new, page_table, write_idx, cu_seqlens, rotary,
+                                         q_out, q, status, stream))
+
+
+def attention_paged_decode_workspace_size(B, Hq, Hkv, D, dtype) -> int:
+    """Bytes of device workspace attention_paged_decode needs (queries the current device)."""
+    dt = EXTKV_F32 if dtype == torch.float32 else EXTKV_BF16
+    return int(load().attention_paged_decode_workspace_size(B, Hq, Hkv, D, dt))
+
+
+def _need_workspace(workspace, need, device, stream):
+    """The caller's workspace, or one from the pool of the stream the call runs
+    on (memory that is given back while the kernels run is then reused behind
+    them)."""
+    if workspace is None:
+        if not need:
+            return None
+        handle = _stream(stream)
+        if handle == torch.cuda.current_stream().cuda_stream:
+            return torch.empty(need, dtype=torch.uint8, device=device)
+        with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0)):
+            return torch.empty(need, dtype=torch.uint8, device=device)
+    _need(workspace, "workspace")
+    return workspace
+
+
+def _ws_bytes(workspace) -> int:
+    return 0 if workspace is None else workspace.numel() * workspace.element_size()
+
+
+def _marshal_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window, workspace, status, stream):
+    if q.dim() != 3:
+        raise ValueError(f"q must have 3 dims, got {tuple(q.shape)}")
+    B, Hq, D = q.shape
+    qs = _need_rows(q, "q", (B, Hq, D), q.dtype)
+    _need(y, "y", dims=3, dtype=q.dtype)
+    _need_pages(k_pages, v_pages, page_table, B, q.dtype)
+    _need(nonpad, "nonpad", dims=1, dtype=torch.int64)
+    num_pages, Hkv, page_size, Dk = k_pages.shape
+    if y.shape != q.shape or Dk != D or nonpad.shape[0] != B:
+        raise ValueError("inconsistent q / y / pages / nonpad shapes")
+    _need_status(status)
+    dt = _dt(q)
+    _on_current_device(y=y, q=q, k_pages=k_pages, v_pages=v_pages, page_table=page_table, nonpad=nonpad,
+                       workspace=workspace, status=status)
+    workspace = _need_workspace(workspace, attention_paged_decode_workspace_size(B, Hq, Hkv, D, q.dtype), q.device,
+                                stream)
+    return load().attention_paged_decode, (_p(y), _p(q), _p(k_pages), _p(v_pages), _p(page_table), _p(nonpad),
+                                           float(scale), int(window), B, Hq, Hkv, D, num_pages, page_size,
+                                           page_table.shape[1], qs, dt, _p(workspace), _ws_bytes(workspace),
+                                           _p(status), _stream(stream)), \
+        (workspace, y, q, k_pages, v_pages, page_table, nonpad, status)
+
+
+def attention_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window: int = 0, workspace=None,
+                           status=None, stream=None):
+    """Attention of one new token per sequence, q (B,Hq,D), over its first
+    ``nonpad[b]`` slots (the last ``window`` of them when window > 0) in the
+    pages (num_pages,Hkv,page_size,D); writes ``y`` (B,Hq,D).  The workspace is
+    allocated here when not given (a call that is recorded into a step needs one
+    that lives as long as the step)."""
+    fn, args, _ = _marshal_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window, workspace, status,
+                                        stream)
+    _check(fn(*args))
+
+
+def prepare_attention_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window: int = 0,
+                                   workspace=None, status=None, stream=None) -> PreparedCall:
+    """attention_paged_decode with its arguments marshalled once (PreparedCall)."""
+    return PreparedCall(*_marshal_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window, workspace,
+                                               status, stream))
+
+
+def attention_packed_prefill_workspace_size(T, B, Hq, Hkv, D, dtype) -> int:
+    """Bytes of device workspace attention_packed_prefill needs (queries the current device)."""
+    dt = EXTKV_F32 if dtype == torch.float32 else EXTKV_BF16
+    return int(load().attention_packed_prefill_workspace_size(T, B, Hq, Hkv, D, dt))
+
+
+def _marshal_packed_prefill(y, q, k, v, cu_seqlens, scale, causal, window, workspace, status, stream):
+    for t, n in ((q, "q"), (k, "k")):
+        if t.dim() != 3:
+            raise ValueError(f"{n} must have 3 dims, got {tuple(t.shape)}")
+    T, Hq, D = q.shape
+    Hkv = k.shape[1]
+    qs = _need_rows(q, "q", (T, Hq, D), q.dtype)
+    ks = _need_rows(k, "k", (T, Hkv, D), q.dtype)
+    vs = _need_rows(v, "v", (T, Hkv, D), q.dtype)
+    _need(y, "y", dims=3, dtype=q.dtype)
+    if y.shape != q.shape:
+        raise ValueError("y must have q's shape")
+    _need(cu_seqlens, "cu_seqlens", dims=1, dtype=torch.int64)
+    if cu_seqlens.shape[0] < 1:
+        raise ValueError("cu_seqlens must have B + 1 entries")
+    B = cu_seqlens.shape[0] - 1
+    _need_status(status)
+    dt = _dt(q)
+    _on_current_device(y=y, q=q, k=k, v=v, cu_seqlens=cu_seqlens, workspace=workspace, status=status)
+    workspace = _need_workspace(workspace, attention_packed_prefill_workspace_size(T, B, Hq, Hkv, D, q.dtype),
+                                q.device, stream)
+    return load().attention_packed_prefill, (_p(y), _p(q), _p(k), _p(v), _p(cu_seqlens), float(scale),
+                                             int(bool(causal)), int(window), T, B, Hq, Hkv, D, qs, ks, vs, dt,
+                                             _p(workspace), _ws_bytes(workspace), _p(status), _stream(stream)), \
+        (workspace, y, q, k, v, cu_seqlens, status)
+
+
+def attention_packed_prefill(y, q, k, v, cu_seqlens, scale, causal: bool = True, window: int = 0, workspace=None,
+                             status=None, stream=None):
+    """Attention over whole prompts packed one after another: q (T,Hq,D),
+    k, v (T,Hkv,D), sequence b in rows cu_seqlens[b]..cu_seqlens[b+1]-1; writes
+    the sequences' rows of ``y`` (T,Hq,D).  q, k and v may have any row stride
+    that is a multiple of 16 bytes.  The workspace is allocated here when not
+    given (a call that is recorded into a step needs one that lives as long as
+    the step)."""
+    fn, args, _ = _marshal_packed_prefill(y, q, k, v, cu_seqlens, scale, causal, window, workspace, status, stream)
+    _check(fn(*args))
+
+
+def prepare_attention_packed_prefill(y, q, k, v, cu_seqlens, scale, causal: bool = True, window: int = 0,
+                                     workspace=None, status=None, stream=None) -> PreparedCall:
+    """attention_packed_prefill with its arguments marshalled once (PreparedCall)."""
+    return PreparedCall(*_marshal_packed_prefill(y, q, k, v, cu_seqlens, scale, causal, window, workspace, status,
+                                                 stream))
 
 
 def new_status(device="cuda") -> torch.Tensor:

@@ -72,6 +72,8 @@ typedef enum {
 #define EXTKV_DEV_BOUNDS 0x8        /* a library built with EXTKV_CHECKED skipped a global access whose
                                        index fell outside its buffer (device bounds checks in place
                                        of a sanitizer: no trap, no fault) */
+#define EXTKV_DEV_BAD_PAGE 0x10     /* a page table entry that a call needed is outside [0, num_pages) */
+#define EXTKV_DEV_BAD_SEQLENS 0x20  /* cu_seqlens descends or leaves [0, T] */
 
 /*
  * The bias specification of mobius issue #366 (deliverable: causal + sliding
@@ -304,6 +306,140 @@ int attention_ext_kv_noalloc(void *y, const void *q, const void *k_cache, const 
                              const int64_t *nonpad, float scale, int64_t B, int64_t Hq,
                              int64_t Hkv, int64_t S_q, int64_t max_seq, int64_t D, int dtype,
                              int32_t *status, void *stream);
+
+/* ---- sequences packed one after another, and a cache in pages --------------------
+ *
+ * Serving batches sequences of very different lengths.  Two layouts serve them
+ * beside the dense ones above:
+ *   packed rows   (T, H, D): the rows of all sequences one after another.  Rows
+ *                 cu_seqlens[b] .. cu_seqlens[b+1]-1 belong to sequence b;
+ *                 cu_seqlens is (B+1,) int64 on the device, 0 <= cu_seqlens[0],
+ *                 ascending (equal neighbours: an empty sequence), its last
+ *                 value <= T.  Rows outside every sequence are neither read into
+ *                 a result nor written.  A cu_seqlens that breaks these rules is
+ *                 flagged EXTKV_DEV_BAD_SEQLENS (see each call for what it then
+ *                 writes).  The rows of a tensor are dense, (H, D); successive
+ *                 rows are `stride` elements apart (>= H * D, a multiple of 16
+ *                 bytes), so q, k and v may be slices of one projection's output.
+ *   pages         k_pages, v_pages (num_pages, Hkv, page_size, D): slot j of
+ *                 sequence b is row j % page_size of page
+ *                 page_table[b, j / page_size]; page_table is (B, max_pages) int64
+ *                 on the device.  Entries of pages that a call does not need are
+ *                 not looked at; a needed one outside [0, num_pages) is flagged
+ *                 EXTKV_DEV_BAD_PAGE and its slots are skipped.  Sequences may
+ *                 share pages that are only read.  page_size is any positive
+ *                 number; num_pages * Hkv * page_size < 2^32 - 1.
+ */
+
+/*
+ * Rotary positions with several axes (time, height and width of an image's or
+ * a video's patches; one axis for text).  The first rotary_dim elements of
+ * every head are turned in pairs, pair i by the angle
+ *     positions[axis(i), row] * inv_freq[i],      i < rotary_dim / 2
+ * where axis(i) is the axis whose section holds i: sections[0] pairs belong to
+ * axis 0, the next sections[1] to axis 1, and so on.  Pair i is elements
+ * (i, i + rotary_dim/2), or (2i, 2i + 1) when `interleaved` is not 0:
+ *     (a, b) -> (a cos - b sin, b cos + a sin)
+ * The other elements pass unchanged.  Far positions lose nothing: the angle is
+ * formed in fixed-point turns, which wrap as angles do, and errs by
+ * |position * inv_freq| * 2^-95 turns at most before it is rounded to fp32;
+ * sine, cosine and the turn are fp32, rounded once to the element type.
+ * |inv_freq| < 2^32 (a pair of any other frequency becomes NaN).
+ * n_axes is 1 to 4; the sections sum to rotary_dim / 2; rotary_dim is even,
+ * 2 <= rotary_dim <= D.  positions is (n_axes, rows) int64 and inv_freq
+ * (rotary_dim / 2) float32, both on the device; the struct is read on the host
+ * during the call.
+ */
+typedef struct {
+  int32_t n_axes;
+  int32_t sections[4];
+  int32_t rotary_dim;
+  int32_t interleaved;
+  const int64_t *positions;
+  const float *inv_freq;
+} extkv_rotary;
+
+/*
+ * Rotates q (B,Hq,S,D) into q_out and k (B,Hkv,S,D) into k_out (dense, BNSH:
+ * the layouts attention_ext_kv and ext_kv_scatter take).  positions is
+ * (n_axes, B, S).  Either pair may be NULL; q_out == q and k_out == k rotate
+ * in place (no other overlap).  Requires D * sizeof(T) % 16 == 0, D <= 512 and
+ * 16-byte aligned tensors.
+ */
+int rotary_multi_axis(void *q_out, void *k_out, const void *q, const void *k, const extkv_rotary *rotary, int64_t B,
+                      int64_t Hq, int64_t Hkv, int64_t S, int64_t D, int dtype, void *stream);
+
+/*
+ * Writes the packed new rows k_new, v_new (T,Hkv,D) into the cache's pages:
+ * row t of sequence b goes to slot write_idx[b] + t - cu_seqlens[b].
+ * cu_seqlens NULL: one row per sequence (T == B), the rows of a decode step.
+ * With `rotary` (positions (n_axes, T)) the K rows are rotated on the way, and
+ * so are the rows of q (T,Hq,D) into q_out (dense; q_out == q with a dense q
+ * rotates in place) when q is given; V rows are copied.  Without it both are
+ * bit-exact copies and q must be NULL.
+ * A sequence whose rows would leave [0, max_pages * page_size) is not written
+ * and flagged EXTKV_DEV_BAD_WRITE_IDX; a row whose page is outside the pool is
+ * not written and flagged EXTKV_DEV_BAD_PAGE (its q row is rotated all the
+ * same).  After EXTKV_DEV_BAD_SEQLENS rows may be missing; nothing is written
+ * that a valid row would not write.  No two rows of a call may share a slot.
+ * Requires D * sizeof(T) % 16 == 0, D <= 512, 16-byte aligned tensors.
+ */
+int paged_kv_append(void *k_pages, void *v_pages, const void *k_new, const void *v_new, const int64_t *page_table,
+                    const int64_t *write_idx, const int64_t *cu_seqlens, void *q_out, const void *q,
+                    const extkv_rotary *rotary, int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D,
+                    int64_t num_pages, int64_t page_size, int64_t max_pages, int64_t q_stride, int64_t k_stride,
+                    int64_t v_stride, int dtype, int32_t *status, void *stream);
+
+/*
+ * Attention of one new token per sequence over its pages:
+ *     y[b,h] = softmax_j(scale * q[b,h] . K[j]) V[j],  j over sequence b's slots
+ *     [0, nonpad[b]), or with window > 0 its last `window` of them
+ * (the token sits at position nonpad[b] - 1, its own K/V row already in the
+ * pages).  q has B rows (Hq,D), q_stride elements apart; y is dense (B,Hq,D).
+ * Query head h reads KV head h / (Hq/Hkv).  Statistics, products' sums and the
+ * joining of split sequences are fp32; the result does not depend on timing.
+ *   - nonpad[b] == 0 gives zero rows; nonpad outside [0, max_pages * page_size]
+ *     too, flagged EXTKV_DEV_BAD_NONPAD.  Slots outside the range never reach
+ *     the result, whatever they hold (NaN included); neither do those of a bad
+ *     page (EXTKV_DEV_BAD_PAGE), and a row left without keys is a zero row.
+ *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
+ *     max_pages * page_size < 2^31.
+ *   - bf16 with D in {64,128,256,512} runs on tensor cores, every other shape
+ *     on fp32 SIMT; both split the batch's keys evenly over the GPU.
+ * workspace: attention_paged_decode_workspace_size(...) bytes, 256-byte
+ * aligned, as for attention_ext_kv (calls that can overlap need their own).
+ */
+int attention_paged_decode(void *y, const void *q, const void *k_pages, const void *v_pages,
+                           const int64_t *page_table, const int64_t *nonpad, float scale, int32_t window, int64_t B,
+                           int64_t Hq, int64_t Hkv, int64_t D, int64_t num_pages, int64_t page_size,
+                           int64_t max_pages, int64_t q_stride, int dtype, void *workspace, size_t ws_bytes,
+                           int32_t *status, void *stream);
+size_t attention_paged_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype);
+
+/*
+ * Attention over whole prompts packed one after another: row i of a sequence
+ * attends the rows j of the same sequence with
+ *     (!causal || j <= i) and (window <= 0 || i - j < window)
+ *     y[i,h] = softmax_j(scale * q[i,h] . k[j]) v[j]
+ * q (T,Hq,D), k, v (T,Hkv,D) with row strides, y dense (T,Hq,D); query head h
+ * reads KV head h / (Hq/Hkv).  Rows of y outside every sequence are left as
+ * they were.  After EXTKV_DEV_BAD_SEQLENS nothing is written.
+ *   - Rows of other sequences never reach a result, whatever they hold.  A row
+ *     of v that holds an infinity or a NaN may reach every row of its own
+ *     sequence, as 0 * infinity does.
+ *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
+ *     T < 2^31 - 256.
+ *   - bf16 with D in {64,128,256} runs on the tcgen05 tensor cores, every other
+ *     shape on fp32 SIMT.  P is rounded to bf16 for the P.V product there (its
+ *     sum is taken before that).
+ * workspace: attention_packed_prefill_workspace_size(...) bytes, 256-byte
+ * aligned, as for attention_ext_kv (calls that can overlap need their own).
+ */
+int attention_packed_prefill(void *y, const void *q, const void *k, const void *v, const int64_t *cu_seqlens,
+                             float scale, int32_t causal, int32_t window, int64_t T, int64_t B, int64_t Hq,
+                             int64_t Hkv, int64_t D, int64_t q_stride, int64_t k_stride, int64_t v_stride, int dtype,
+                             void *workspace, size_t ws_bytes, int32_t *status, void *stream);
+size_t attention_packed_prefill_workspace_size(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype);
 
 /* Zeroes the 16-byte status word on `stream` (asynchronous). */
 int extkv_clear_status(int32_t *status, void *stream);
