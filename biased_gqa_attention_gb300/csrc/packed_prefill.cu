@@ -5,6 +5,7 @@
 
 #include "internal.h"
 #include "packed_plan.cuh"
+#include "packed_tc.h"
 #include "simt_tile.cuh"
 #include "tma_host.h"
 
@@ -214,12 +215,27 @@ int pack_heads(int64_t g, int cap) {
   return pk;
 }
 
+// Rows of a work item and the query heads packed into it.  The tensor-core
+// kernel's query tiles are M = 128 rows.
+struct Shape {
+  bool tc;
+  int rows, pk;
+};
+
+Shape shape_of(int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
+  Shape s;
+  s.tc = packed_tc_supported(D, dtype);
+  s.rows = s.tc ? packed_tc_rows(D) : kTileRows;
+  s.pk = pack_heads(Hq / Hkv, s.tc ? 128 : kTileRows);
+  return s;
+}
+
+int64_t max_items(const Shape& s, int64_t T, int64_t B) { return T / (s.rows / s.pk) + B + 1; }
+
 }  // namespace
 
 size_t packed_workspace_bytes(int64_t T, int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
-  const int pk = pack_heads(Hq / Hkv, kTileRows);
-  const int64_t items = T * pk / kTileRows + B + 1;
-  return 256 + ((items * sizeof(PackedItem) + 255) & ~size_t(255));
+  return 256 + ((max_items(shape_of(Hq, Hkv, D, dtype), T, B) * sizeof(PackedItem) + 255) & ~size_t(255));
 }
 
 cudaError_t launch_packed(const PackedArgs& a, const char** name) {
@@ -241,10 +257,11 @@ cudaError_t launch_packed(const PackedArgs& a, const char** name) {
   p.q_stride = a.q_stride;
   p.k_stride = a.k_stride;
   p.v_stride = a.v_stride;
-  p.pk = pack_heads(p.g, kTileRows);
-  p.tile_tok = kTileRows / p.pk;
+  const Shape sh = shape_of(a.Hq, a.Hkv, a.D, a.dtype);
+  p.pk = sh.pk;
+  p.tile_tok = sh.rows / sh.pk;
   p.heads = p.Hq / p.pk;
-  p.max_items = static_cast<int>(a.T / p.tile_tok + a.B + 1);
+  p.max_items = static_cast<int>(max_items(sh, a.T, a.B));
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.count = reinterpret_cast<int*>(ws);
   p.items = reinterpret_cast<PackedItem*>(ws + 256);
@@ -253,7 +270,8 @@ cudaError_t launch_packed(const PackedArgs& a, const char** name) {
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, packed_plan_kernel, p);
   if (e != cudaSuccess) return e;
   *name = a.dtype == EXTKV_F32 ? "packed_simt_f32" : "packed_simt_bf16";
-  e = a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);
+  e = sh.tc                    ? launch_packed_tc(p, a.wait_limit_plus1, a.stream, name)
+      : a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);
   if (e == cudaSuccess) note_launches(2);
   return e;
 }

@@ -1,0 +1,502 @@
+// packed_tc.cu -- packed prefill on the 5th-generation tensor cores: bf16, head
+// sizes 64 and 128.
+//
+// Bound: the tensor pipe for long prompts (4 D flops a pair against one
+// exponential a pair), the softmax's instruction rate close behind it.
+//
+// A persistent CTA per SM takes query tiles from the plan's list (dearest
+// first, rounds taken in alternating order).  An item is 256 query rows, two
+// M = 128 tiles A and B of one KV head's (token, head) rows: while one tile's
+// scores go through the softmax, the tensor cores work for the other.
+//   warp 0       loads: Q tiles, then K and V tiles of 128 keys through a ring
+//                of shared-memory units (TMA, 128-byte swizzle)
+//   warp 1       issues the MMAs: for each key tile PV_A(j-1), QK_A(j),
+//                PV_B(j-1), QK_B(j); S and O live in tensor memory, P (bf16)
+//                over the first half of its S
+//   warps 4-7    softmax and output of tile A, a query row per thread
+//   warps 8-11   the same for tile B
+// (warps 2 and 3 only fill the first warpgroup, which gives its registers to
+// the other two: 72 against 216 of the 168 a thread the block starts with.)
+// The tensor pipe runs one thread's MMAs in order, so S_t(j) being complete
+// implies that PV_t(j-1) is: a softmax warp may rescale O_t before it releases
+// P_t(j) without another barrier.  O is rescaled only when a row's maximum has
+// grown by more than 8 in the exponent (P then stays below 2^8, exact enough in
+// bf16 and fp32 alike).
+#include <climits>
+
+#include "internal.h"
+#include "packed_tc.h"
+#include "tma_host.h"
+
+namespace extkv {
+
+namespace {
+
+constexpr int kBM = 128;  // rows of a query tile
+constexpr int kBN = 128;  // keys of a tile
+constexpr uint32_t kWaitPolls = 1u << 22;
+constexpr float kGrow = 8.f;  // log2 units
+constexpr int kMaxUnits = 8;
+
+template <int D>
+struct Cfg {
+  static constexpr int kThreads = 384;
+  static constexpr int kTile = kBM * D * 2;  // bytes of a Q, K or V tile
+  static constexpr int kUnits = (232448 - 2048 - 2 * kTile) / kTile < kMaxUnits ? (232448 - 2048 - 2 * kTile) / kTile : kMaxUnits;
+  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kOffBar = kOffKV + kUnits * kTile;
+  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static constexpr uint32_t kOCol = 256;  // S_A, S_B at 0 and 128; O_A, O_B from here
+  static constexpr uint32_t kTmemCols = 512;
+  static constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0, 0);
+  static constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, D, 0, 1);
+  static_assert(kSmem <= 232448 && kUnits >= 4, "shared memory");
+};
+
+struct Bars {
+  uint64_t q_full[2], q_empty[2];
+  uint64_t u_full[kMaxUnits], u_empty[kMaxUnits];
+  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
+  uint64_t v_tail, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 127u) == 127u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+// Registers of the calling warpgroup; 128 * 72 + 256 * 216 = 384 * 168.
+template <int N>
+__device__ __forceinline__ void reg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void reg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// One entry of the work list for one head group.
+struct Work {
+  int row0, len, tok0, h0, hk;
+  int lo[2], hi[2];  // key tiles of query tiles A and B (empty: tile B has no tokens)
+  int k_lo, k_hi;    // their union
+};
+
+__device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
+  Work r;
+  const int64_t at = w / p.heads;
+  const PackedItem it = p.items[at];
+  r.row0 = it.row0;
+  r.len = it.len;
+  r.tok0 = it.tok0;
+  r.h0 = static_cast<int>(w - at * p.heads) * p.pk;
+  r.hk = r.h0 / p.g;
+  const int tt = p.tile_tok / 2;
+  r.k_lo = INT_MAX;
+  r.k_hi = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int t0 = it.tok0 + t * tt, t1 = min(it.len, t0 + tt);
+    r.lo[t] = r.hi[t] = 0;
+    if (t0 < t1) {
+      r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / kBN;
+      r.hi[t] = ((p.causal ? t1 : it.len) + kBN - 1) / kBN;
+      r.k_lo = min(r.k_lo, r.lo[t]);
+      r.k_hi = max(r.k_hi, r.hi[t]);
+    }
+  }
+  return r;
+}
+
+// Work of this CTA's round i: rounds run over the list back and forth, so that
+// a CTA that got a dear item of one round gets a cheap one of the next.
+__device__ __forceinline__ int64_t work_index(int i) {
+  const int64_t g = gridDim.x;
+  return i * g + ((i & 1) ? g - 1 - blockIdx.x : blockIdx.x);
+}
+
+template <int D>
+__global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
+    packed_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                     const __grid_constant__ CUtensorMap vmap, const PackedParams p) {
+  using C = Cfg<D>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(sm + C::kOffBar);
+  uint8_t* sKV = sm + C::kOffKV;
+  volatile int* abort = &bar.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t lim = p.wait_limit;
+
+  if (tid == 0) {
+    for (int t = 0; t < 2; ++t) {
+      ptx::mbar_init(&bar.q_full[t], 1);
+      ptx::mbar_init(&bar.q_empty[t], 1);
+      ptx::mbar_init(&bar.s_full[t], 1);
+      ptx::mbar_init(&bar.p_full[t], 128);
+      ptx::mbar_init(&bar.o_full[t], 1);
+      ptx::mbar_init(&bar.o_free[t], 128);
+    }
+    for (int u = 0; u < C::kUnits; ++u) {
+      ptx::mbar_init(&bar.u_full[u], 1);
+      ptx::mbar_init(&bar.u_empty[u], 1);
+    }
+    ptx::mbar_init(&bar.v_tail, 1);
+    ptx::mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tensormap(&qmap);
+    ptx::prefetch_tensormap(&kmap);
+    ptx::prefetch_tensormap(&vmap);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&bar.tmem_base, C::kTmemCols);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  const uint32_t tbase = bar.tmem_base;
+  ptx::grid_dependency_wait();  // the plan, and what the caller ran before it
+  const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
+  const int tt = p.tile_tok / 2;
+
+  if (warp < 4) {
+    reg_dec<72>();
+    if (warp == 0) {
+    // ---------------- loads ----------------
+    int u = 0, nq[2] = {0, 0}, tails = 0;
+    bool ok = true;
+    auto acquire = [&]() -> bool {  // the next unit of the ring is free
+      return u < C::kUnits || wait_or_abort(&bar.u_empty[u % C::kUnits], ((u / C::kUnits) - 1) & 1, abort, lim);
+    };
+    auto load_q = [&](const Work& w, int t) -> bool {
+      if (w.lo[t] >= w.hi[t]) return true;
+      if (nq[t] && !wait_or_abort(&bar.q_empty[t], (nq[t] - 1) & 1, abort, lim)) return false;
+      ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kTile);
+      ptx::tma_load_4d(sm + t * C::kTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
+      ++nq[t];
+      return true;
+    };
+    for (int i = 0; ok; ++i) {
+      const int64_t wi = work_index(i);
+      if (wi >= n_work) {
+        if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;  // past the last round
+        continue;
+      }
+      const Work w = work_at(p, wi);
+      if (lane == 0) ok = load_q(w, 0);
+      for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
+        const int key0 = w.row0 + kt * kBN;
+        const bool tail = (kt + 1) * kBN > w.len;  // keys of the next sequence behind the last one
+        if (lane == 0) {
+          ok = ok && acquire();
+          if (ok) {
+            uint64_t* full = &bar.u_full[u % C::kUnits];
+            ptx::mbar_arrive_expect_tx(full, C::kTile);
+            ptx::tma_load_4d(sKV + (u % C::kUnits) * C::kTile, &kmap, full, 0, key0, w.hk, 0);
+          }
+          if (ok && kt == w.k_lo) ok = load_q(w, 1);
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++u;
+        uint8_t* dst = sKV + (u % C::kUnits) * C::kTile;
+        if (lane == 0) {
+          ok = acquire();
+          if (ok) {
+            uint64_t* full = tail ? &bar.v_tail : &bar.u_full[u % C::kUnits];
+            ptx::mbar_arrive_expect_tx(full, C::kTile);
+            ptx::tma_load_4d(dst, &vmap, full, 0, key0, w.hk, 0);
+            if (tail) ok = wait_or_abort(&bar.v_tail, tails & 1, abort, lim);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (tail) {
+          // V rows behind the sequence's last, whatever they hold, become
+          // zeros: their P is 0, and 0 * NaN would be NaN
+          ++tails;
+          constexpr int kPieces = D / 8;  // 16 bytes each
+          for (int x = (w.len - kt * kBN) * kPieces + lane; x < kBN * kPieces; x += 32) {
+            const int r = x / kPieces, ch = x % kPieces;
+            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kBN * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) ptx::mbar_arrive(&bar.u_full[u % C::kUnits]);
+        }
+        ++u;
+      }
+    }
+    if (lane == 0 && *abort) {  // copies still in flight land before the CTA leaves
+      for (int x = u >= C::kUnits ? u - C::kUnits + 1 : 0; x <= u; ++x)
+        ptx::mbar_wait_bounded(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, kWaitPolls >> 6);
+      for (int t = 0; t < 2; ++t)
+        if (nq[t]) ptx::mbar_wait_bounded(&bar.q_full[t], (nq[t] - 1) & 1, kWaitPolls >> 6);
+      ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    if (lane == 0) {
+      const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
+      const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
+      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kBN * 128, 1024);
+      int u = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      bool ok = true, issued = false;
+      // P_t(j) V_j; uv: the unit of V_j; first: of the item
+      auto pv = [&](int t, int uv, bool first) -> bool {
+        if (first && nq[t] > 1 && !wait_or_abort(&bar.o_free[t], (nq[t] - 2) & 1, abort, lim)) return false;
+        if (!wait_or_abort(&bar.p_full[t], np[t] & 1, abort, lim)) return false;
+        ++np[t];
+        ptx::tc_fence_after();
+        const uint64_t vd = vdesc0 + (((uv % C::kUnits) * C::kTile) >> 4);
+#pragma unroll
+        for (int k = 0; k < kBN / 16; ++k)
+          ptx::umma_bf16_ts(tbase + C::kOCol + t * D, tbase + t * kBN + k * 8, vd + ((k * 2048) >> 4), C::kIdescPV,
+                            (!first || k > 0) ? 1u : 0u);
+        return true;
+      };
+      auto qk = [&](int t, int uk) {
+        const uint64_t qd = qdesc0 + ((t * C::kTile) >> 4), kd = kdesc0 + (((uk % C::kUnits) * C::kTile) >> 4);
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+          const uint32_t off = ((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4;
+          ptx::umma_bf16(tbase + t * kBN, qd + off, kd + off, C::kIdescQK, k > 0);
+        }
+        ptx::umma_commit(&bar.s_full[t]);
+      };
+      for (int i = 0; ok; ++i) {
+        const int64_t wi = work_index(i);
+        if (wi >= n_work) {
+          if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;
+          continue;
+        }
+        const Work w = work_at(p, wi);
+        issued = true;
+        for (int t = 0; t < 2; ++t) nq[t] += w.lo[t] < w.hi[t];
+        for (int kt = w.k_lo; kt <= w.k_hi && ok; ++kt) {
+          const int uk = u, uv = u - 1;  // K_kt and V_{kt-1}
+          if (kt < w.k_hi && !(ok = wait_or_abort(&bar.u_full[uk % C::kUnits], (uk / C::kUnits) & 1, abort, lim))) break;
+          if (kt > w.k_lo && !(ok = wait_or_abort(&bar.u_full[uv % C::kUnits], (uv / C::kUnits) & 1, abort, lim))) break;
+          ptx::tc_fence_after();
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (kt - 1 >= w.lo[t] && kt - 1 < w.hi[t]) {
+              if (!(ok = pv(t, uv, kt - 1 == w.lo[t]))) break;
+              if (kt == w.hi[t]) ptx::umma_commit(&bar.o_full[t]);
+            }
+            if (kt >= w.lo[t] && kt < w.hi[t]) {
+              if (kt == w.lo[t] && !(ok = wait_or_abort(&bar.q_full[t], (nq[t] - 1) & 1, abort, lim))) break;
+              ptx::tc_fence_after();
+              qk(t, uk);
+              if (kt == w.hi[t] - 1) ptx::umma_commit(&bar.q_empty[t]);
+            }
+          }
+          if (!ok) break;
+          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[uv % C::kUnits]);
+          if (kt < w.k_hi) ptx::umma_commit(&bar.u_empty[uk % C::kUnits]);
+          u += kt < w.k_hi ? 2 : 0;
+        }
+      }
+      // every MMA issued has completed before tensor memory is released
+      if (issued) {
+        ptx::umma_commit(&bar.drain);
+        if (!ptx::mbar_wait_bounded(&bar.drain, 0, kWaitPolls)) *abort = 1;
+      }
+    }
+    __syncwarp();
+  }
+  } else {
+    // ---------------- softmax and output ----------------
+    reg_inc<216>();
+    const int t = (warp - 4) >> 2;
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tbase + lane_base + t * kBN, to = tbase + lane_base + C::kOCol + t * D;
+    const float c = p.c;
+    const uint64_t c2 = ptx::f2(c, c);
+    int ns = 0, no = 0;
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+      const int64_t wi = work_index(i);
+      if (wi >= n_work) {
+        if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;
+        continue;
+      }
+      const Work w = work_at(p, wi);
+      const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
+      if (lo >= hi) continue;
+      const int tok = w.tok0 + t * tt + row / p.pk;
+      // the row's keys [ra, rb)
+      int ra = p.window > 0 ? max(0, tok - p.window + 1) : 0, rb = p.causal ? tok + 1 : w.len;
+      const bool valid = tok < w.len;
+      if (!valid) ra = rb = 0;
+      float m = -INFINITY, l = 0.f;
+      for (int kt = lo; kt < hi; ++kt) {
+        const int k0 = kt * kBN;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
+          ok = false;
+          break;
+        }
+        ++ns;
+        ptx::tc_fence_after();
+        uint32_t s[4][32];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
+        ptx::tmem_wait_ld();
+        if (!__all_sync(0xffffffffu, ra <= k0 && rb >= k0 + kBN)) {
+          const int a = ra - k0;
+          const unsigned n = rb > ra ? rb - ra : 0;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (static_cast<unsigned>(32 * q + e - a) >= n) s[q][e] = 0xff800000u;
+        }
+        float mt[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float x0 = __uint_as_float(s[q][0]), x1 = __uint_as_float(s[q][1]);
+#pragma unroll
+          for (int e = 2; e < 32; e += 4) {
+            x0 = ptx::max3(x0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+            if (e + 3 < 32) x1 = ptx::max3(x1, __uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]));
+          }
+          mt[q] = fmaxf(x0, x1);
+        }
+        const float m_new = fmaxf(m, ptx::max3(mt[0], mt[1], fmaxf(mt[2], mt[3])));
+        const bool grow = (m_new - m) * c > kGrow;  // false while the row has no key (NaN)
+        const bool first = m == -INFINITY;
+        if (__any_sync(0xffffffffu, grow && !first)) {
+          // PV_t(kt - 1) is complete (S_t(kt) was issued after it)
+          const float f = grow && !first ? ptx::ex2((m - m_new) * c) : 1.f;
+          l *= f;
+#pragma unroll 1
+          for (int q = 0; q < D / 32; ++q) {
+            uint32_t o[32];
+            ptx::tmem_ld32(to + 32 * q, o);
+            ptx::tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+            ptx::tmem_st32(to + 32 * q, o);
+          }
+        }
+        if (grow) m = m_new;
+        const float nm = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t nm2 = ptx::f2(nm, nm);
+        uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+        for (int hf = 0; hf < 2; ++hf) {
+          // P rounded to bf16 for the product; l sums the unrounded weights
+          uint32_t pk[32];
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const uint32_t* sp = &s[2 * hf + (x >> 4)][2 * (x & 15)];
+            const uint64_t d = ptx::fma2(ptx::f2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, nm2);
+            const float e0 = ptx::ex2(ptx::f2_lo(d)), e1 = ptx::ex2(ptx::f2_hi(d));
+            ls[x & 3] = ptx::add2(ls[x & 3], ptx::f2(e0, e1));
+            pk[x] = ptx::pack_bf16x2(e0, e1);
+          }
+          ptx::tmem_st32(ts + 32 * hf, pk);
+        }
+        const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+        l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
+        ptx::tmem_wait_st();
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.p_full[t]);
+      }
+      if (!ok) break;
+      if (!__all_sync(0xffffffffu, wait_or_abort(&bar.o_full[t], no & 1, abort, lim))) {
+        ok = false;
+        break;
+      }
+      ++no;
+      ptx::tc_fence_after();
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
+      const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y0;
+#pragma unroll
+      for (int q = 0; q < D / 64; ++q) {
+        uint32_t o[2][32];
+        ptx::tmem_ld32(to + 64 * q, o[0]);
+        ptx::tmem_ld32(to + 64 * q + 32, o[1]);
+        ptx::tmem_wait_ld();
+        if (q == D / 64 - 1) {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bar.o_free[t]);
+        }
+        if (in) {
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            uint32_t v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int k = 8 * x + 2 * e;
+              v[e] = ptx::pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
+            }
+            *reinterpret_cast<uint4*>(y + 64 * q + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
+          }
+        }
+      }
+    }
+  }
+  ptx::grid_launch_dependents();
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::tc_fence_after();
+  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);
+  if (warp == 1) ptx::tmem_dealloc(tbase, C::kTmemCols);
+}
+
+template <int D>
+cudaError_t launch(const PackedParams& p, cudaStream_t s) {
+  using C = Cfg<D>;
+  CUtensorMap qmap, kmap, vmap;
+  const uint64_t T = p.T, chunks = D / 64;
+  const uint32_t tt = p.tile_tok / 2;
+  // (64 columns, head, row, 64-column chunk): a box lands a tile's (token, head)
+  // rows one after another
+  const uint64_t q_dims[4] = {64, static_cast<uint64_t>(p.Hq), T, chunks};
+  const uint64_t q_str[3] = {D * 2, static_cast<uint64_t>(p.q_stride) * 2, 128};
+  const uint32_t q_box[4] = {64, static_cast<uint32_t>(p.pk), tt, static_cast<uint32_t>(chunks)};
+  const uint64_t k_dims[4] = {64, T, static_cast<uint64_t>(p.Hkv), chunks};
+  const uint64_t k_str[3] = {static_cast<uint64_t>(p.k_stride) * 2, D * 2, 128};
+  const uint64_t v_str[3] = {static_cast<uint64_t>(p.v_stride) * 2, D * 2, 128};
+  const uint32_t k_box[4] = {64, kBN, 1, static_cast<uint32_t>(chunks)};
+  if (!make_tensor_map_bf16(&qmap, p.q, 4, q_dims, q_str, q_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tensor_map_bf16(&kmap, p.k, 4, k_dims, k_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tensor_map_bf16(&vmap, p.v, 4, k_dims, v_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  auto k = packed_tc_kernel<D>;
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), C::kSmem); e != cudaSuccess) return e;
+  const int64_t work = static_cast<int64_t>(p.max_items) * p.heads;
+  PdlLaunch l(dim3(static_cast<unsigned>(work < num_sms() ? work : num_sms())), C::kThreads, C::kSmem, s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, qmap, kmap, vmap, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace
+
+bool packed_tc_supported(int64_t D, int dtype) { return dtype == EXTKV_BF16 && (D == 64 || D == 128); }
+
+int packed_tc_rows(int64_t D) { return 2 * kBM; }
+
+cudaError_t launch_packed_tc(PackedParams& p, uint32_t wait_limit_plus1, cudaStream_t s, const char** name) {
+  *name = "packed_tcgen05";
+  p.wait_limit = wait_limit(wait_limit_plus1, kWaitPolls);
+  return p.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
+}
+
+}  // namespace extkv

@@ -63,6 +63,11 @@ __device__ __forceinline__ int tiles_of(LiveKeys k) {
   return (k.hi - k.lo + KT - 1) / KT;
 }
 
+// Slices the axis is cut into: one per warp, or one per tile when there are fewer.
+__device__ __forceinline__ int live_slices(const PagedParams& p, int64_t total) {
+  return total < p.slices ? static_cast<int>(total) : p.slices;
+}
+
 // A position on the axis of tiles.
 template <int KT>
 struct Cursor {
@@ -212,10 +217,11 @@ __global__ void __launch_bounds__(C::WARPS * 32, 1) paged_decode_mma_kernel(cons
   ptx::grid_launch_dependents();
   const int per = scan_tiles<KT>(p, pre, warp_sum);
   const int64_t total = pre[blockDim.x] * p.units;
-  const int slice = blockIdx.x * C::WARPS + warp;
-  const int64_t f0 = total * slice / p.slices, f1 = total * (slice + 1) / p.slices;
-  const int n = static_cast<int>(f1 - f0);
-  if (n == 0) return;
+  const int slice = warp * gridDim.x + blockIdx.x;  // few tiles: one warp per SM first
+  const int slices = live_slices(p, total);
+  if (slice >= slices) return;
+  const int64_t f0 = total * slice / slices, f1 = total * (slice + 1) / slices;
+  const int n = static_cast<int>(f1 - f0);  // at least one
 
   const uint32_t ring = ptx::smem_u32(smem) + warp * ST * C::kStage;
   Cursor<KT> ld = cursor_at<KT>(p, pre, per, f0);
@@ -458,10 +464,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
   ptx::grid_launch_dependents();
   const int per = scan_tiles<KT>(p, pre, warp_sum);
   const int64_t total = pre[blockDim.x] * p.units;
-  const int slice = blockIdx.x * kSimtWarps + warp;
-  const int64_t f0 = total * slice / p.slices, f1 = total * (slice + 1) / p.slices;
-  const int n = static_cast<int>(f1 - f0);
-  if (n == 0) return;
+  const int slice = warp * gridDim.x + blockIdx.x;
+  const int slices = live_slices(p, total);
+  if (slice >= slices) return;
+  const int64_t f0 = total * slice / slices, f1 = total * (slice + 1) / slices;
+  const int n = static_cast<int>(f1 - f0);  // at least one
 
   const int stride = simt_stride<T>(D);
   const int stage = 2 * KT * stride;  // elements
@@ -575,74 +582,108 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
 
 // ---- joining the units split over slices -----------------------------------------------
 
-constexpr int kMergeWarps = 4;
-
 // One CTA per (sequence, query head).  A unit's partials lie in the slices that
 // hold its tiles: the first of them may have ended an earlier unit before it
-// (then its partial is in the second place), the others begin with it.  Warps
-// take every fourth slice, their sums are added in order.
+// (then its partial is in the second place), the others begin with it.  The
+// slices' weights exp2(max_s - M) go to shared memory; then a thread owns four
+// columns and every kSub-th slice, eight loads in flight, and the kSub sums are
+// added in order.
+constexpr int kMergeThreads = 256;
+constexpr int kMaxSlices = 2048;
+
 template <typename T>
-__global__ void __launch_bounds__(kMergeWarps * 32) paged_merge_kernel(const PagedParams p) {
-  __shared__ float acc_s[kMergeWarps][512];
-  __shared__ float red[2][kMergeWarps];
+__global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedParams p) {
+  __shared__ float w_s[kMaxSlices];
+  __shared__ float4 acc_s[kMergeThreads];
+  __shared__ float red[2][kMergeThreads / 32];
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x - b * p.Hq, D = p.D;
   const int hk = h / p.g, hr = h - hk * p.g, gr = hr / p.rows, r = hr - gr * p.rows;
   const int64_t b0 = p.base[b], tiles = p.base[b + 1] - b0, total = p.base[p.B] * p.units;
   T* y = static_cast<T*>(p.y) + (static_cast<int64_t>(b) * p.Hq + h) * D;
   if (tiles == 0) {  // no key
-    for (int d = threadIdx.x; d < D; d += kMergeWarps * 32) y[d] = Elem<T>::from_float(0.f);
+    for (int d = tid; d < D; d += kMergeThreads) y[d] = Elem<T>::from_float(0.f);
     return;
   }
+  const int slices = live_slices(p, total);
   const int64_t u0 = b0 * p.units + static_cast<int64_t>(hk * p.groups + gr) * tiles;
   // the slice that holds tile f is the last whose first tile is <= f
-  const int s0 = static_cast<int>(((u0 + 1) * p.slices - 1) / total);
-  const int s1 = static_cast<int>(((u0 + tiles) * p.slices - 1) / total);
+  const int s0 = static_cast<int>(((u0 + 1) * slices - 1) / total);
+  const int s1 = static_cast<int>(((u0 + tiles) * slices - 1) / total);
   if (s0 == s1) return;  // written by the slice itself
-  const int first_slot = total * s0 / p.slices < u0 ? 1 : 0;
-  // slices between the first and the last can be empty of tiles when there are fewer tiles than slices
-  auto holds = [&](int s) { return total * (s + 1) / p.slices > total * s / p.slices; };
-  auto at = [&](int s) { return (static_cast<int64_t>(s) * 2 + (s == s0 ? first_slot : 0)) * p.rows + r; };
+  const int first_slot = total * s0 / slices < u0 ? 1 : 0;
+  const int n = s1 - s0 + 1;
+  // partial i of the unit, in rows of the workspace
+  auto at = [&](int i) { return (static_cast<int64_t>(s0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.rows + r; };
 
   float M = -INFINITY;
-  for (int s = s0 + threadIdx.x; s <= s1; s += kMergeWarps * 32)
-    if (holds(s)) M = fmaxf(M, __ldcg(&p.ml[at(s)].x));
+  for (int i = tid; i < n; i += kMergeThreads) {
+    const float m = __ldcg(&p.ml[at(i)].x);
+    w_s[i] = m;
+    M = fmaxf(M, m);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   if (lane == 0) red[0][warp] = M;
   __syncthreads();
-  M = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+#pragma unroll
+  for (int i = 0; i < kMergeThreads / 32; ++i) M = fmaxf(M, red[0][i]);
   const float ref = M == -INFINITY ? 0.f : M;
-
-  float L = 0.f, acc[16];
-#pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
-  for (int s = s0 + warp; s <= s1; s += kMergeWarps) {
-    if (!holds(s)) continue;
-    const float2 ml = __ldcg(&p.ml[at(s)]);
-    if (ml.x == -INFINITY && ml.y == 0.f) continue;  // every key of the slice was skipped
-    const float w = ptx::ex2(ml.x - ref);
-    L = fmaf(w, ml.y, L);
-    const float* src = p.part + at(s) * D;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const int d = lane + 32 * i;
-      if (d < D) acc[i] = fmaf(w, __ldcg(src + d), acc[i]);
-    }
+  float L = 0.f;
+  for (int i = tid; i < n; i += kMergeThreads) {
+    const float w = w_s[i] == -INFINITY ? 0.f : ptx::ex2(w_s[i] - ref);  // -inf: every key of the slice was skipped
+    w_s[i] = w;
+    L = fmaf(w, __ldcg(&p.ml[at(i)].y), L);
   }
-  if (lane == 0) red[1][warp] = L;
 #pragma unroll
-  for (int i = 0; i < 16; ++i) {
-    const int d = lane + 32 * i;
-    if (d < D) acc_s[warp][d] = acc[i];
+  for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
+  if (lane == 0) red[1][warp] = L;
+  __syncthreads();
+  L = 0.f;
+#pragma unroll
+  for (int i = 0; i < kMergeThreads / 32; ++i) L += red[1][i];
+
+  const int cols = D / 4, subs = kMergeThreads / cols;  // D <= 512: two at least
+  const int sub = tid / cols, c = tid - sub * cols;
+  float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (sub < subs) {
+    auto add = [&](int i, const float4& v) {
+      const float w = w_s[i];
+      a.x = fmaf(w, v.x, a.x);
+      a.y = fmaf(w, v.y, a.y);
+      a.z = fmaf(w, v.z, a.z);
+      a.w = fmaf(w, v.w, a.w);
+    };
+    const float4* part = reinterpret_cast<const float4*>(p.part) + c;
+    int i = sub;
+    for (; i + 7 * subs < n; i += 8 * subs) {
+      float4 v[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) v[u] = __ldcg(part + at(i + u * subs) * cols);
+#pragma unroll
+      for (int u = 0; u < 8; ++u) add(i + u * subs, v[u]);
+    }
+    for (; i < n; i += subs) add(i, __ldcg(part + at(i) * cols));
+    acc_s[tid] = a;
   }
   __syncthreads();
-  L = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-  const float inv = L != 0.f ? 1.f / L : 0.f;
-  for (int d = threadIdx.x; d < D; d += kMergeWarps * 32)
-    y[d] = Elem<T>::from_float(((acc_s[0][d] + acc_s[1][d]) + (acc_s[2][d] + acc_s[3][d])) * inv);
+  if (sub == 0) {
+    for (int u = 1; u < subs; ++u) {
+      const float4 v = acc_s[u * cols + c];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    const float inv = L != 0.f ? 1.f / L : 0.f;
+    T* yc = y + 4 * c;
+    yc[0] = Elem<T>::from_float(a.x * inv);
+    yc[1] = Elem<T>::from_float(a.y * inv);
+    yc[2] = Elem<T>::from_float(a.z * inv);
+    yc[3] = Elem<T>::from_float(a.w * inv);
+  }
 }
 
 // ---- host ------------------------------------------------------------------------------
@@ -669,7 +710,7 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   pl.rows = unit_rows(g, D, mma);
   pl.groups = static_cast<int>((g + pl.rows - 1) / pl.rows);
   pl.warps = mma ? mma_warps(D) : kSimtWarps;
-  pl.slices = num_sms() * pl.warps;
+  pl.slices = std::min(num_sms() * pl.warps, kMaxSlices / pl.warps * pl.warps);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   pl.off_ml = up(sizeof(int64_t) * (B + 1));
   pl.off_part = pl.off_ml + up(sizeof(float2) * 2 * pl.slices * pl.rows);
@@ -708,7 +749,7 @@ cudaError_t launch_simt_d(const PagedParams& p, cudaStream_t s) {
 
 template <typename T>
 cudaError_t launch_merge(const PagedParams& p, cudaStream_t s) {
-  PdlLaunch l(dim3(static_cast<unsigned>(p.B * p.Hq)), kMergeWarps * 32, 0, s);
+  PdlLaunch l(dim3(static_cast<unsigned>(p.B * p.Hq)), kMergeThreads, 0, s);
   cudaError_t e = cudaLaunchKernelEx(&l.cfg, paged_merge_kernel<T>, p);
   return e != cudaSuccess ? e : cudaGetLastError();
 }

@@ -203,3 +203,19 @@ def test_other_stream_and_captured():
     graphs[1].replay()
     torch.cuda.synchronize()
     assert torch.equal(outs[1][0], run(q, k, v, cu, 0.1, True, 0))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_a_wait_that_runs_out_is_reported(D):
+    """A poll limit of zero: the pipeline's waits give up, the status word says so,
+    and the next call is whole again."""
+    q, k, v, cu = make((300, 77), 4, 2, D, torch.bfloat16)
+    y = torch.full_like(q, 7.0)
+    st = ek.new_status()
+    with ek.wait_polls(0):
+        ek.attention_packed_prefill(y, q, k, v, cu, 0.1, status=st)
+        assert "tcgen05" in ek.extkv_last_kernel()
+    assert ek.extkv_read_status(st) == ek.EXTKV_ERR_DEVICE and int(st[0]) == ek.EXTKV_DEV_TIMEOUT
+    y = run(q, k, v, cu, 0.1, True, 0)
+    ref, tol = reference(q, k, v, cu, 0.1, True, 0)
+    check(y, ref, tol, "after")
