@@ -225,7 +225,7 @@ struct Shape {
 Shape shape_of(int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   Shape s;
   s.tc = packed_tc_supported(D, dtype);
-  s.rows = s.tc ? packed_tc_rows(D) : kTileRows;
+  s.rows = s.tc ? kPackedTcRows : kTileRows;
   s.pk = pack_heads(Hq / Hkv, s.tc ? 128 : kTileRows);
   return s;
 }

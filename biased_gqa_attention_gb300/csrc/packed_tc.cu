@@ -22,9 +22,8 @@
 // P_t(j) without another barrier.  O is rescaled only when a row's maximum has
 // grown by more than 8 in the exponent (P then stays below 2^8, exact enough in
 // bf16 and fp32 alike).
-#include <climits>
-
 #include "internal.h"
+#include "packed_tc.cuh"
 #include "packed_tc.h"
 #include "tma_host.h"
 
@@ -32,10 +31,8 @@ namespace extkv {
 
 namespace {
 
-constexpr int kBM = 128;  // rows of a query tile
-constexpr int kBN = 128;  // keys of a tile
-constexpr uint32_t kWaitPolls = 1u << 22;
-constexpr float kGrow = 8.f;  // log2 units
+using namespace packed;
+
 constexpr int kMaxUnits = 8;
 
 template <int D>
@@ -63,15 +60,6 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
-  for (uint32_t i = 0; i < limit; ++i) {
-    if (ptx::mbar_try_wait(bar, parity)) return true;
-    if ((i & 127u) == 127u && *abort) return false;
-  }
-  *abort = 1;
-  return false;
-}
-
 // Registers of the calling warpgroup; 128 * 72 + 256 * 216 = 384 * 168.
 template <int N>
 __device__ __forceinline__ void reg_dec() {
@@ -80,46 +68,6 @@ __device__ __forceinline__ void reg_dec() {
 template <int N>
 __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-// One entry of the work list for one head group.
-struct Work {
-  int row0, len, tok0, h0, hk;
-  int lo[2], hi[2];  // key tiles of query tiles A and B (empty: tile B has no tokens)
-  int k_lo, k_hi;    // their union
-};
-
-__device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
-  Work r;
-  const int64_t at = w / p.heads;
-  const PackedItem it = p.items[at];
-  r.row0 = it.row0;
-  r.len = it.len;
-  r.tok0 = it.tok0;
-  r.h0 = static_cast<int>(w - at * p.heads) * p.pk;
-  r.hk = r.h0 / p.g;
-  const int tt = p.tile_tok / 2;
-  r.k_lo = INT_MAX;
-  r.k_hi = 0;
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int t0 = it.tok0 + t * tt, t1 = min(it.len, t0 + tt);
-    r.lo[t] = r.hi[t] = 0;
-    if (t0 < t1) {
-      r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / kBN;
-      r.hi[t] = ((p.causal ? t1 : it.len) + kBN - 1) / kBN;
-      r.k_lo = min(r.k_lo, r.lo[t]);
-      r.k_hi = max(r.k_hi, r.hi[t]);
-    }
-  }
-  return r;
-}
-
-// Work of this CTA's round i: rounds run over the list back and forth, so that
-// a CTA that got a dear item of one round gets a cheap one of the next.
-__device__ __forceinline__ int64_t work_index(int i) {
-  const int64_t g = gridDim.x;
-  return i * g + ((i & 1) ? g - 1 - blockIdx.x : blockIdx.x);
 }
 
 template <int D>
@@ -187,12 +135,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ++nq[t];
       return true;
     };
-    for (int i = 0; ok; ++i) {
-      const int64_t wi = work_index(i);
-      if (wi >= n_work) {
-        if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;  // past the last round
-        continue;
-      }
+    Rounds rounds(n_work, blockIdx.x, gridDim.x);
+    for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
       const Work w = work_at(p, wi);
       if (lane == 0) ok = load_q(w, 0);
       for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
@@ -217,22 +161,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             uint64_t* full = tail ? &bar.v_tail : &bar.u_full[u % C::kUnits];
             ptx::mbar_arrive_expect_tx(full, C::kTile);
             ptx::tma_load_4d(dst, &vmap, full, 0, key0, w.hk, 0);
-            if (tail) ok = wait_or_abort(&bar.v_tail, tails & 1, abort, lim);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         if (tail) {
-          // V rows behind the sequence's last, whatever they hold, become
-          // zeros: their P is 0, and 0 * NaN would be NaN
+          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_tail, tails & 1, abort, lim)))) break;
           ++tails;
-          constexpr int kPieces = D / 8;  // 16 bytes each
-          for (int x = (w.len - kt * kBN) * kPieces + lane; x < kBN * kPieces; x += 32) {
-            const int r = x / kPieces, ch = x % kPieces;
-            *reinterpret_cast<uint4*>(dst + (ch >> 3) * (kBN * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
-          }
-          ptx::fence_proxy_async_smem();
-          __syncwarp();
+          zero_rows<D>(dst, w.len - kt * kBN, kBN, lane);
           if (lane == 0) ptx::mbar_arrive(&bar.u_full[u % C::kUnits]);
         }
         ++u;
@@ -276,12 +212,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         ptx::umma_commit(&bar.s_full[t]);
       };
-      for (int i = 0; ok; ++i) {
-        const int64_t wi = work_index(i);
-        if (wi >= n_work) {
-          if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;
-          continue;
-        }
+      Rounds rounds(n_work, blockIdx.x, gridDim.x);
+      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at(p, wi);
         issued = true;
         for (int t = 0; t < 2; ++t) nq[t] += w.lo[t] < w.hi[t];
@@ -325,15 +257,10 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const uint32_t ts = tbase + lane_base + t * kBN, to = tbase + lane_base + C::kOCol + t * D;
     const float c = p.c;
-    const uint64_t c2 = ptx::f2(c, c);
     int ns = 0, no = 0;
     bool ok = true;
-    for (int i = 0; ok; ++i) {
-      const int64_t wi = work_index(i);
-      if (wi >= n_work) {
-        if (wi - (i & 1 ? gridDim.x - 1 - blockIdx.x : blockIdx.x) >= n_work) break;
-        continue;
-      }
+    Rounds rounds(n_work, blockIdx.x, gridDim.x);
+    for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
       const Work w = work_at(p, wi);
       const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
       if (lo >= hi) continue;
@@ -351,68 +278,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         }
         ++ns;
         ptx::tc_fence_after();
-        uint32_t s[4][32];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
-        ptx::tmem_wait_ld();
-        if (!__all_sync(0xffffffffu, ra <= k0 && rb >= k0 + kBN)) {
-          const int a = ra - k0;
-          const unsigned n = rb > ra ? rb - ra : 0;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (static_cast<unsigned>(32 * q + e - a) >= n) s[q][e] = 0xff800000u;
-        }
-        float mt[4];
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          float x0 = __uint_as_float(s[q][0]), x1 = __uint_as_float(s[q][1]);
-#pragma unroll
-          for (int e = 2; e < 32; e += 4) {
-            x0 = ptx::max3(x0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-            if (e + 3 < 32) x1 = ptx::max3(x1, __uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]));
-          }
-          mt[q] = fmaxf(x0, x1);
-        }
-        const float m_new = fmaxf(m, ptx::max3(mt[0], mt[1], fmaxf(mt[2], mt[3])));
-        const bool grow = (m_new - m) * c > kGrow;  // false while the row has no key (NaN)
-        const bool first = m == -INFINITY;
-        if (__any_sync(0xffffffffu, grow && !first)) {
-          // PV_t(kt - 1) is complete (S_t(kt) was issued after it)
-          const float f = grow && !first ? ptx::ex2((m - m_new) * c) : 1.f;
-          l *= f;
-#pragma unroll 1
-          for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            ptx::tmem_ld32(to + 32 * q, o);
-            ptx::tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-            ptx::tmem_st32(to + 32 * q, o);
-          }
-        }
-        if (grow) m = m_new;
-        const float nm = m == -INFINITY ? 0.f : -m * c;
-        const uint64_t nm2 = ptx::f2(nm, nm);
-        uint64_t ls[4] = {0, 0, 0, 0};
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          // P rounded to bf16 for the product; l sums the unrounded weights
-          uint32_t pk[32];
-#pragma unroll
-          for (int x = 0; x < 32; ++x) {
-            const uint32_t* sp = &s[2 * hf + (x >> 4)][2 * (x & 15)];
-            const uint64_t d = ptx::fma2(ptx::f2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, nm2);
-            const float e0 = ptx::ex2(ptx::f2_lo(d)), e1 = ptx::ex2(ptx::f2_hi(d));
-            ls[x & 3] = ptx::add2(ls[x & 3], ptx::f2(e0, e1));
-            pk[x] = ptx::pack_bf16x2(e0, e1);
-          }
-          ptx::tmem_st32(ts + 32 * hf, pk);
-        }
-        const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
-        l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
-        ptx::tmem_wait_st();
+        // PV_t(kt - 1) is complete: S_t(kt) was issued after it
+        softmax_tile<D>(ts, to, ra, rb, k0, c, m, l, [] { return true; });
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.p_full[t]);
       }
@@ -423,33 +290,12 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       }
       ++no;
       ptx::tc_fence_after();
-      const float inv = l != 0.f ? 1.f / l : 0.f;
       const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
       const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
-      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y0;
-#pragma unroll
-      for (int q = 0; q < D / 64; ++q) {
-        uint32_t o[2][32];
-        ptx::tmem_ld32(to + 64 * q, o[0]);
-        ptx::tmem_ld32(to + 64 * q + 32, o[1]);
-        ptx::tmem_wait_ld();
-        if (q == D / 64 - 1) {
-          ptx::tc_fence_before();
-          ptx::mbar_arrive(&bar.o_free[t]);
-        }
-        if (in) {
-#pragma unroll
-          for (int x = 0; x < 8; ++x) {
-            uint32_t v[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const int k = 8 * x + 2 * e;
-              v[e] = ptx::pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
-            }
-            *reinterpret_cast<uint4*>(y + 64 * q + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
-          }
-        }
-      }
+      store_row<D>(to, l, in, static_cast<__nv_bfloat16*>(p.y) + y0, [&] {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.o_free[t]);
+      });
     }
   }
   ptx::grid_launch_dependents();
@@ -489,13 +335,12 @@ cudaError_t launch(const PackedParams& p, cudaStream_t s) {
 
 }  // namespace
 
-bool packed_tc_supported(int64_t D, int dtype) { return dtype == EXTKV_BF16 && (D == 64 || D == 128); }
-
-int packed_tc_rows(int64_t D) { return 2 * kBM; }
+bool packed_tc_supported(int64_t D, int dtype) { return dtype == EXTKV_BF16 && (D == 64 || D == 128 || D == 256); }
 
 cudaError_t launch_packed_tc(PackedParams& p, uint32_t wait_limit_plus1, cudaStream_t s, const char** name) {
   *name = "packed_tcgen05";
   p.wait_limit = wait_limit(wait_limit_plus1, kWaitPolls);
+  if (p.D == 256) return launch_packed_tc_d256(p, s);
   return p.D == 64 ? launch<64>(p, s) : launch<128>(p, s);
 }
 

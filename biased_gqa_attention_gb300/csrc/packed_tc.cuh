@@ -1,0 +1,193 @@
+// packed_tc.cuh -- device parts shared by the tensor-core packed prefill kernels.
+#pragma once
+
+#include <climits>
+
+#include "packed_plan.cuh"
+
+namespace extkv {
+namespace packed {
+
+constexpr int kBM = 128;  // rows of a query tile
+constexpr int kBN = 128;  // keys of a tile
+constexpr uint32_t kWaitPolls = 1u << 22;
+constexpr float kGrow = 8.f;  // log2 units
+
+// Bounded wait that also gives up once another role has aborted.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  for (uint32_t i = 0; i < limit; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 127u) == 127u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+// One entry of the work list for one head group: two query tiles of
+// tile_tok / 2 tokens each.
+struct Work {
+  int row0, len, tok0, h0, hk;
+  int lo[2], hi[2];  // key tiles of query tiles A and B (empty: tile B has no tokens)
+  int k_lo, k_hi;    // their union
+};
+
+__device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
+  Work r;
+  const int64_t at = w / p.heads;
+  const PackedItem it = p.items[at];
+  r.row0 = it.row0;
+  r.len = it.len;
+  r.tok0 = it.tok0;
+  r.h0 = static_cast<int>(w - at * p.heads) * p.pk;
+  r.hk = r.h0 / p.g;
+  const int tt = p.tile_tok / 2;
+  r.k_lo = INT_MAX;
+  r.k_hi = 0;
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int t0 = it.tok0 + t * tt, t1 = min(it.len, t0 + tt);
+    r.lo[t] = r.hi[t] = 0;
+    if (t0 < t1) {
+      r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / kBN;
+      r.hi[t] = ((p.causal ? t1 : it.len) + kBN - 1) / kBN;
+      r.k_lo = min(r.k_lo, r.lo[t]);
+      r.k_hi = max(r.k_hi, r.hi[t]);
+    }
+  }
+  return r;
+}
+
+// The work of worker `id` of `n`: rounds run over the list back and forth, so
+// that a worker that got a dear item of one round gets a cheap one of the next.
+struct Rounds {
+  int64_t base = 0, n_work;
+  int id, n, odd = 0;
+  __device__ __forceinline__ Rounds(int64_t n_work_, int id_, int n_) : n_work(n_work_), id(id_), n(n_) {}
+  // the next item, or -1
+  __device__ __forceinline__ int64_t next() {
+    const int64_t w = base + (odd ? n - 1 - id : id);
+    base += n;
+    odd ^= 1;
+    return w < n_work ? w : -1;  // only the last round is short
+  }
+};
+
+// The softmax of one query row over one key tile: reads its 128 scores (raw
+// q.k) from tensor memory at `ts`, writes P (bf16) over the first 64 columns,
+// keeps the row's maximum m (raw) and sum l, and rescales the row of O at `to`
+// (D columns) when the maximum has grown by more than kGrow, so that P stays
+// below 2^8.  [ra, rb): the row's keys; k0: the tile's first; c: scale * log2(e).
+// `o_ready` is asked before O is rescaled: the product that last wrote it must
+// be complete (false: that wait gave up, and so does this).
+template <int D, class F>
+__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, int ra, int rb, int k0, float c, float& m,
+                                             float& l, F o_ready) {
+  uint32_t s[4][32];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
+  ptx::tmem_wait_ld();
+  if (!__all_sync(0xffffffffu, ra <= k0 && rb >= k0 + kBN)) {
+    const int a = ra - k0;
+    const unsigned n = rb > ra ? rb - ra : 0;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        if (static_cast<unsigned>(32 * q + e - a) >= n) s[q][e] = 0xff800000u;
+  }
+  float mt[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    float x0 = __uint_as_float(s[q][0]), x1 = __uint_as_float(s[q][1]);
+#pragma unroll
+    for (int e = 2; e < 32; e += 4) {
+      x0 = ptx::max3(x0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+      if (e + 3 < 32) x1 = ptx::max3(x1, __uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]));
+    }
+    mt[q] = fmaxf(x0, x1);
+  }
+  const float m_new = fmaxf(m, ptx::max3(mt[0], mt[1], fmaxf(mt[2], mt[3])));
+  const bool grow = (m_new - m) * c > kGrow;  // false while the row has no key (NaN)
+  const bool first = m == -INFINITY;
+  if (__any_sync(0xffffffffu, grow && !first)) {
+    if (!o_ready()) return false;
+    const float f = grow && !first ? ptx::ex2((m - m_new) * c) : 1.f;
+    l *= f;
+#pragma unroll 1
+    for (int q = 0; q < D / 32; ++q) {
+      uint32_t o[32];
+      ptx::tmem_ld32(to + 32 * q, o);
+      ptx::tmem_wait_ld();
+#pragma unroll
+      for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+      ptx::tmem_st32(to + 32 * q, o);
+    }
+  }
+  if (grow) m = m_new;
+  const float nm = m == -INFINITY ? 0.f : -m * c;
+  const uint64_t c2 = ptx::f2(c, c), nm2 = ptx::f2(nm, nm);
+  uint64_t ls[4] = {0, 0, 0, 0};
+#pragma unroll
+  for (int hf = 0; hf < 2; ++hf) {
+    // P rounded to bf16 for the product (2^-8 of each weight at most); l sums
+    // the unrounded weights
+    uint32_t pk[32];
+#pragma unroll
+    for (int x = 0; x < 32; ++x) {
+      const uint32_t* sp = &s[2 * hf + (x >> 4)][2 * (x & 15)];
+      const uint64_t d = ptx::fma2(ptx::f2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, nm2);
+      const float e0 = ptx::ex2(ptx::f2_lo(d)), e1 = ptx::ex2(ptx::f2_hi(d));
+      ls[x & 3] = ptx::add2(ls[x & 3], ptx::f2(e0, e1));
+      pk[x] = ptx::pack_bf16x2(e0, e1);
+    }
+    ptx::tmem_st32(ts + 32 * hf, pk);
+  }
+  const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+  l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
+  ptx::tmem_wait_st();
+  return true;
+}
+
+// One row of O at `to` over its sum l, into y (D columns) when `in`; `release`
+// runs once the row has been read.
+template <int D, class F>
+__device__ __forceinline__ void store_row(uint32_t to, float l, bool in, __nv_bfloat16* y, F release) {
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+#pragma unroll
+  for (int q = 0; q < D / 64; ++q) {
+    uint32_t o[2][32];
+    ptx::tmem_ld32(to + 64 * q, o[0]);
+    ptx::tmem_ld32(to + 64 * q + 32, o[1]);
+    ptx::tmem_wait_ld();
+    if (q == D / 64 - 1) release();
+    if (in) {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 8 * x + 2 * e;
+          v[e] = ptx::pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
+        }
+        *reinterpret_cast<uint4*>(y + 64 * q + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+}
+
+// Zeroes V rows [r0, n) of a tile stored as 64-column chunks of n rows (128-byte
+// swizzled rows; a whole row is zeroed, so the swizzle does not matter): rows
+// behind a sequence's last have P = 0, but 0 * NaN would be NaN.
+template <int D>
+__device__ __forceinline__ void zero_rows(uint8_t* tile, int r0, int n, int lane) {
+  constexpr int kPieces = D / 8;  // 16 bytes each
+  for (int x = r0 * kPieces + lane; x < n * kPieces; x += 32) {
+    const int r = x / kPieces, ch = x % kPieces;
+    *reinterpret_cast<uint4*>(tile + (ch >> 3) * (n * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  ptx::fence_proxy_async_smem();  // before the tensor cores read them
+  __syncwarp();
+}
+
+}  // namespace packed
+}  // namespace extkv

@@ -1,0 +1,331 @@
+// packed_tc_d256.cu -- packed prefill on the 5th-generation tensor cores for
+// head size 256.
+//
+// Tensor memory holds S_0, S_1 (128 columns each) and one O (256 columns), so a
+// CTA has one M = 128 query tile; the scores of key tile j + 1 are computed
+// while tile j goes through the softmax.  A K and a V tile are 64 KB each for
+// 2240 tensor cycles: 58 bytes a cycle and SM from L2, about all it gives.  So
+// two CTAs form a cluster and take the two query tiles of one item (the same
+// keys): each loads half of every unit and multicasts it to both, which halves
+// the reads.
+//   warp 0     loads: its Q tile; its half of each 32 KB unit of K (128 keys by
+//              128 columns) and V (64 keys by 256 columns)
+//   warp 1     issues the MMAs: QK(j+1), PV(j)
+//   warps 2-5  softmax and output, a query row per thread
+// A unit's slot is refilled when both CTAs' MMAs have read it (their commits
+// arrive in both CTAs).
+#include "internal.h"
+#include "packed_tc.cuh"
+#include "packed_tc.h"
+#include "tma_host.h"
+
+namespace extkv {
+
+namespace {
+
+using namespace packed;
+
+constexpr int D = 256;
+constexpr int kThreads = 192;
+constexpr int kUnits = 5;
+constexpr int kUnit = 32768;
+constexpr int kQBytes = kBM * D * 2;
+constexpr int kOffKV = kQBytes;
+constexpr int kOffBar = kOffKV + kUnits * kUnit;
+constexpr int kSmem = kOffBar + 512 + 1024;
+constexpr uint32_t kOCol = 256;
+constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0, 0);
+constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, D, 0, 1);
+constexpr uint16_t kBoth = 3;
+static_assert(kSmem <= 232448, "shared memory");
+
+struct Bars {
+  uint64_t q_full, q_empty;
+  uint64_t u_full[kUnits], u_empty[kUnits], v_land[kUnits];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t o_full, o_free, drain;
+  uint32_t tmem_base;
+  int abort;
+};
+static_assert(sizeof(Bars) <= 512, "barrier block");
+
+__global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
+    packed_tc_d256_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
+                          const __grid_constant__ CUtensorMap vmap, const PackedParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  // the same offset in both CTAs: their windows start alike
+  uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  Bars& bar = *reinterpret_cast<Bars*>(sm + kOffBar);
+  uint8_t* sKV = sm + kOffKV;
+  volatile int* abort = &bar.abort;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t lim = p.wait_limit;
+  const int rank = static_cast<int>(ptx::cluster_ctarank());
+
+  if (tid == 0) {
+    ptx::mbar_init(&bar.q_full, 1);
+    ptx::mbar_init(&bar.q_empty, 1);
+    for (int u = 0; u < kUnits; ++u) {
+      ptx::mbar_init(&bar.u_full[u], 1);
+      ptx::mbar_init(&bar.u_empty[u], 2);
+      ptx::mbar_init(&bar.v_land[u], 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      ptx::mbar_init(&bar.s_full[s], 1);
+      ptx::mbar_init(&bar.p_full[s], 128);
+      ptx::mbar_init(&bar.pv_done[s], 1);
+    }
+    ptx::mbar_init(&bar.o_full, 1);
+    ptx::mbar_init(&bar.o_free, 128);
+    ptx::mbar_init(&bar.drain, 1);
+    bar.abort = 0;
+    ptx::fence_mbar_init();
+  }
+  if (warp == 0 && lane == 0) {
+    ptx::prefetch_tensormap(&qmap);
+    ptx::prefetch_tensormap(&kmap);
+    ptx::prefetch_tensormap(&vmap);
+  }
+  if (warp == 1) {
+    ptx::tmem_alloc(&bar.tmem_base, 512);
+    ptx::tmem_relinquish();
+  }
+  ptx::tc_fence_before();
+  __syncthreads();
+  ptx::cluster_sync();  // the peer's barriers exist before anything arrives on them
+  ptx::tc_fence_after();
+  const uint32_t tbase = bar.tmem_base;
+  ptx::grid_dependency_wait();
+  const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
+  const int tt = p.tile_tok / 2;
+  Rounds rounds(n_work, blockIdx.x / 2, gridDim.x / 2);
+  int armed = 0;       // warp 0: units whose barriers expect bytes
+  uint32_t tails = 0;  // warp 0: phase of each unit's v_land
+
+  if (warp == 0) {
+    // ---------------- loads ----------------
+    int u = 0, nq = 0;
+    bool ok = true;
+    // the next unit: its slot is free in both CTAs, the barrier is armed, this CTA's half on its way to both
+    auto load = [&](const CUtensorMap* map, bool tail, int32_t row, int32_t hk, int32_t chunk, int half_bytes) -> bool {
+      const int s = u % kUnits;
+      if (lane == 0) {
+        ok = u < kUnits || wait_or_abort(&bar.u_empty[s], ((u / kUnits) - 1) & 1, abort, lim);
+        if (ok) {
+          uint64_t* full = tail ? &bar.v_land[s] : &bar.u_full[s];
+          ptx::mbar_arrive_expect_tx(full, kUnit);
+          ptx::tma_load_4d_multicast(sKV + s * kUnit + rank * half_bytes, map, full, 0, row, hk, chunk, kBoth);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, ok, 0);
+      if (!ok) return false;
+      armed = u + 1;
+      return true;
+    };
+    auto load_k = [&](const Work& w, int kt) -> bool {
+      for (int part = 0; part < 2; ++part, ++u)  // 128 columns; this CTA's half is one 64-column chunk
+        if (!load(&kmap, false, w.row0 + kt * kBN, w.hk, 2 * part + rank, kUnit / 2)) return false;
+      return true;
+    };
+    auto load_v = [&](const Work& w, int kt) -> bool {
+      for (int part = 0; part < 2; ++part, ++u) {  // 64 keys; this CTA's half is two chunks
+        const int k0 = kt * kBN + part * 64, s = u % kUnits;
+        const bool tail = k0 + 64 > w.len;
+        if (!load(&vmap, tail, w.row0 + k0, w.hk, 2 * rank, kUnit / 2)) return false;
+        if (tail) {
+          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_land[s], (tails >> s) & 1, abort, lim)))) return false;
+          tails ^= 1u << s;
+          zero_rows<D>(sKV + s * kUnit, max(0, w.len - k0), 64, lane);
+          if (lane == 0) ptx::mbar_arrive(&bar.u_full[s]);
+        }
+      }
+      return true;
+    };
+    for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+      const Work w = work_at(p, wi);
+      const bool active = rank ? w.lo[1] < w.hi[1] : w.lo[0] < w.hi[0];
+      if (active) {
+        if (lane == 0) {
+          ok = !nq || wait_or_abort(&bar.q_empty, (nq - 1) & 1, abort, lim);
+          if (ok) {
+            ptx::mbar_arrive_expect_tx(&bar.q_full, kQBytes);
+            ptx::tma_load_4d(sm, &qmap, &bar.q_full, 0, w.h0, w.row0 + w.tok0 + rank * tt, 0);
+          }
+        }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        ++nq;
+      }
+      if (!load_k(w, w.k_lo)) break;
+      for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
+        if (kt + 1 < w.k_hi && !load_k(w, kt + 1)) break;
+        load_v(w, kt);
+      }
+    }
+    if (lane == 0 && *abort && nq) ptx::mbar_wait_bounded(&bar.q_full, (nq - 1) & 1, kWaitPolls >> 6);
+    __syncwarp();
+  } else if (warp == 1) {
+    // ---------------- MMAs ----------------
+    if (lane == 0) {
+      const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
+      const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
+      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 64 * 128, 1024);
+      int u = 0, nq = 0, cq = 0, cp = 0;  // units, items, QK and PV products issued
+      bool ok = true, issued = false;
+      // the two units of a K or V tile, in load order
+      auto qk = [&](bool active, bool first) -> bool {
+        for (int part = 0; part < 2; ++part, ++u) {
+          const int s = u % kUnits;
+          if (!wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
+          ptx::tc_fence_after();
+          if (active) {
+            if (first && part == 0) {
+              if (!wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim)) return false;
+              ptx::tc_fence_after();
+            }
+            const uint64_t kd = kdesc0 + ((s * kUnit) >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const uint64_t qd = qdesc0 + (((2 * part + (k >> 2)) * (kBM * 128) + (k & 3) * 32) >> 4);
+              ptx::umma_bf16(tbase + (cq & 1) * kBN, qd, kd + (((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4), kIdescQK,
+                             part > 0 || k > 0);
+            }
+          }
+          ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
+        }
+        if (active) {
+          ptx::umma_commit(&bar.s_full[cq & 1]);
+          ++cq;
+        }
+        return true;
+      };
+      auto pv = [&](bool active, bool first) -> bool {
+        for (int part = 0; part < 2; ++part, ++u) {
+          const int s = u % kUnits;
+          if (!wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
+          if (active) {
+            if (part == 0) {
+              if (first && nq > 1 && !wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim)) return false;
+              if (!wait_or_abort(&bar.p_full[cp & 1], (cp >> 1) & 1, abort, lim)) return false;
+            }
+            ptx::tc_fence_after();
+            const uint64_t vd = vdesc0 + ((s * kUnit) >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              ptx::umma_bf16_ts(tbase + kOCol, tbase + (cp & 1) * kBN + (part * 4 + k) * 8, vd + ((k * 2048) >> 4),
+                                kIdescPV, !first || part > 0 || k > 0);
+          }
+          ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
+        }
+        if (active) {
+          ptx::umma_commit(&bar.pv_done[cp & 1]);
+          ++cp;
+        }
+        return true;
+      };
+      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+        const Work w = work_at(p, wi);
+        const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
+        issued = true;
+        nq += lo < hi;
+        auto act = [&](int kt) { return kt >= lo && kt < hi; };
+        ok = qk(act(w.k_lo), w.k_lo == lo);
+        for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
+          if (kt + 1 < w.k_hi && !(ok = qk(act(kt + 1), kt + 1 == lo))) break;
+          if (kt + 1 == hi - 1 || (kt == w.k_lo && kt == hi - 1)) ptx::umma_commit(&bar.q_empty);
+          if (!(ok = pv(act(kt), kt == lo))) break;
+          if (kt == hi - 1) ptx::umma_commit(&bar.o_full);
+        }
+      }
+      if (issued) {
+        ptx::umma_commit(&bar.drain);
+        if (!ptx::mbar_wait_bounded(&bar.drain, 0, kWaitPolls)) *abort = 1;
+      }
+    }
+    __syncwarp();
+  } else {
+    // ---------------- softmax and output ----------------
+    const int row = 32 * (warp & 3) + lane;
+    const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
+    const uint32_t ts = tbase + lane_base, to = ts + kOCol;
+    int n = 0, no = 0;
+    bool ok = true;
+    for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+      const Work w = work_at(p, wi);
+      const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
+      if (lo >= hi) continue;
+      const int tok = w.tok0 + rank * tt + row / p.pk;
+      const bool valid = tok < w.len;
+      int ra = p.window > 0 ? max(0, tok - p.window + 1) : 0, rb = p.causal ? tok + 1 : w.len;
+      if (!valid) ra = rb = 0;
+      float m = -INFINITY, l = 0.f;
+      for (int kt = lo; kt < hi; ++kt, ++n) {
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
+        ptx::tc_fence_after();
+        ok = softmax_tile<D>(ts + (n & 1) * kBN, to, ra, rb, kt * kBN, p.c, m, l, [&] {
+          const bool done =
+              __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, lim));
+          ptx::tc_fence_after();
+          return done;
+        });
+        if (!ok) break;
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.p_full[n & 1]);
+      }
+      if (!ok || !(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.o_full, no & 1, abort, lim)))) break;
+      ++no;
+      ptx::tc_fence_after();
+      const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
+      const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
+      store_row<D>(to, l, in, static_cast<__nv_bfloat16*>(p.y) + y0, [&] {
+        ptx::tc_fence_before();
+        ptx::mbar_arrive(&bar.o_free);
+      });
+    }
+  }
+  ptx::grid_launch_dependents();
+  ptx::tc_fence_before();
+  __syncthreads();
+  // Neither CTA leaves while the other's copies or commits may still reach it:
+  // after the first meeting nothing more is issued, then (only after an abort)
+  // what this CTA's barriers were armed for lands or was never sent.
+  ptx::cluster_sync();
+  if (warp == 0 && lane == 0 && *abort) {
+    for (int x = armed > kUnits ? armed - kUnits : 0; x < armed; ++x) {
+      ptx::mbar_wait_bounded(&bar.u_full[x % kUnits], (x / kUnits) & 1, kWaitPolls >> 6);
+      ptx::mbar_wait_bounded(&bar.v_land[x % kUnits], (tails >> (x % kUnits)) & 1, kWaitPolls >> 8);
+    }
+  }
+  __syncwarp();
+  ptx::cluster_sync();
+  ptx::tc_fence_after();
+  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);
+  if (warp == 1) ptx::tmem_dealloc(tbase, 512);
+}
+
+}  // namespace
+
+cudaError_t launch_packed_tc_d256(const PackedParams& p, cudaStream_t s) {
+  CUtensorMap qmap, kmap, vmap;
+  const uint64_t T = p.T, chunks = D / 64;
+  const uint32_t tt = p.tile_tok / 2;
+  const uint64_t q_dims[4] = {64, static_cast<uint64_t>(p.Hq), T, chunks};
+  const uint64_t q_str[3] = {D * 2, static_cast<uint64_t>(p.q_stride) * 2, 128};
+  const uint32_t q_box[4] = {64, static_cast<uint32_t>(p.pk), tt, static_cast<uint32_t>(chunks)};
+  const uint64_t k_dims[4] = {64, T, static_cast<uint64_t>(p.Hkv), chunks};
+  const uint64_t k_str[3] = {static_cast<uint64_t>(p.k_stride) * 2, D * 2, 128};
+  const uint64_t v_str[3] = {static_cast<uint64_t>(p.v_stride) * 2, D * 2, 128};
+  const uint32_t k_box[4] = {64, kBN, 1, 1}, v_box[4] = {64, 64, 1, 2};
+  if (!make_tensor_map_bf16(&qmap, p.q, 4, q_dims, q_str, q_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tensor_map_bf16(&kmap, p.k, 4, k_dims, k_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+      !make_tensor_map_bf16(&vmap, p.v, 4, k_dims, v_str, v_box, CU_TENSOR_MAP_SWIZZLE_128B))
+    return cudaErrorInvalidValue;
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(packed_tc_d256_kernel), kSmem); e != cudaSuccess)
+    return e;
+  const int64_t work = static_cast<int64_t>(p.max_items) * p.heads, clusters = num_sms() / 2;
+  PdlLaunch l(dim3(static_cast<unsigned>(2 * (work < clusters ? work : clusters))), kThreads, kSmem, s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, packed_tc_d256_kernel, qmap, kmap, vmap, p);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+}  // namespace extkv
