@@ -23,9 +23,16 @@ namespace extkv {
 
 namespace {
 
+// Measured (GB300, the copy rate is 6.78 TB/s): 8194 rows of 24 heads of 256,
+// 192 of each turned, 201 MB: 38 us, 5.3 TB/s; 8144 rows of q, K and V (32 + 2 +
+// 2 heads of 128) into pages, 150 MB: 30 us, 5.0 TB/s.  One wave of CTAs beats
+// more and smaller ones (4 rows a CTA: 36 us on the second), two vectors a
+// thread with five CTAs beat four with four (41 us on the first), and
+// prefetching the rows to L2 before the angles costs 3 us.
 constexpr int kThreads = 256;
-constexpr int kMaxRows = 8;  // rows per CTA
-constexpr int kUnroll = 4;   // vectors in flight per thread
+constexpr int kMaxRows = 16;  // rows per CTA
+constexpr int kUnroll = 2;   // vectors in flight per thread
+constexpr int kMinCtas = 5;
 
 struct Tensor {
   const void* src;
@@ -120,6 +127,13 @@ __device__ __forceinline__ void pack(Vec<T, VW>& x, const float (&f)[VW]) {
   }
 }
 
+// x / d for x and d below 2^16.
+struct SmallDiv {
+  uint32_t d, inv;
+  __device__ __forceinline__ explicit SmallDiv(int d_) : d(d_), inv(d_ > 1 ? 0xffffffffu / d_ + 1 : 0) {}
+  __device__ __forceinline__ int operator()(int x) const { return d > 1 ? __umulhi(x, inv) : x; }
+};
+
 // Where a row goes; -1: nowhere.
 struct RowPlace {
   int64_t q_src, q_dst, k_src, k_dst, v_src, v_dst;
@@ -128,8 +142,8 @@ struct RowPlace {
 // VW: elements per access (16 bytes, or 1 where a half of the rotated part is
 // not whole vectors).  INTER: pairs (2i, 2i+1); else (i, i + R/2).
 template <typename T, int VW, bool INTER>
-__global__ void __launch_bounds__(kThreads) rotary_append_kernel(const RotaryParams p) {
-  extern __shared__ float2 cs[];  // [rows][R/2]
+__global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const RotaryParams p) {
+  extern __shared__ float2 cs[];  // [rows][PV][R/2 / PV]
   __shared__ RowPlace place[kMaxRows];
   const int tid = threadIdx.x;
   const int64_t row0 = static_cast<int64_t>(blockIdx.x) * p.rows_per_cta;
@@ -138,13 +152,17 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(const RotaryPar
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
 
+  // angle i of a vector's PV pairs, vector by vector, so that the threads of a
+  // warp, which hold neighbouring vectors, read neighbouring words
+  constexpr int PV = VW == 1 ? 1 : INTER ? VW / 2 : VW;
+  const int n_vec = half / PV;
   for (int i = tid; i < rows * half; i += kThreads) {
     const int r = i / half, c = i - r * half;
     int axis = 0;
 #pragma unroll
     for (int a = 0; a < 3; ++a) axis += c >= p.sec_end[a] ? 1 : 0;
     axis = min(axis, p.n_axes - 1);
-    cs[i] = cos_sin(p.positions[axis * p.n_rows + row0 + r], p.inv_freq[c]);
+    cs[r * half + (c % PV) * n_vec + c / PV] = cos_sin(p.positions[axis * p.n_rows + row0 + r], p.inv_freq[c]);
   }
   if (tid >= kThreads - rows) {  // one of the last threads per row: its source and destination
     const int r = tid - (kThreads - rows);
@@ -208,109 +226,108 @@ __global__ void __launch_bounds__(kThreads) rotary_append_kernel(const RotaryPar
   }
   __syncthreads();
 
-  // items of one (row, head): R/2 / VW pair vectors (interleaved: R / VW whole
-  // vectors; single elements: R/2 pairs), then the unrotated vectors
-  const int rot = INTER && VW > 1 ? p.R / VW : half / VW;
-  const int per_head = rot + (p.D - p.R) / VW;  // q and k
-  const int per_v = p.D / VW;
   const int h0 = blockIdx.y * p.heads_per_cta;
   const int h1 = min(h0 + p.heads_per_cta, p.q.heads + p.k.heads + p.v.heads);
   const int hv = p.q.heads + p.k.heads;  // first head of v
-  const int nr = max(0, min(h1, hv) - h0), nv = max(0, h1 - max(h0, hv));
-  const int per_row = nr * per_head + nv * per_v;
-  const int total = rows * per_row;
-
-  struct Item {
-    const T* s;
-    T* d;
-    int part;  // distance of the pair's other vector; 0: none
-    int cs;    // first angle; -1: a copy
-  };
-  auto item_at = [&](int i) -> Item {
-    const int r = i / per_row;
-    int x = i - r * per_row;
-    Item it{nullptr, nullptr, 0, -1};
-    const RowPlace& pl = place[r];
-    if (x < nr * per_head) {
-      const int hh = x / per_head, c = x - hh * per_head, h = h0 + hh;
-      const bool is_q = h < p.q.heads;
-      const Tensor& t = is_q ? p.q : p.k;
-      const int hd = is_q ? h : h - p.q.heads;
-      const int64_t so = (is_q ? pl.q_src : pl.k_src) + hd * t.sh, dr = is_q ? pl.q_dst : pl.k_dst;
-      if (dr < 0) return it;
-      int e;
-      if (c >= rot) {
-        e = p.R + (c - rot) * VW;
-      } else if (INTER && VW > 1) {
-        e = c * VW;
-        it.cs = r * half + c * (VW / 2);
-      } else {
-        e = INTER ? 2 * c : c * VW;
-        it.part = INTER ? 1 : half;
-        it.cs = r * half + c * VW;
-      }
-      const int64_t d_at = dr + hd * t.dh + e;
-      if (!EXTKV_IN(d_at, VW, is_q ? p.q_total : p.k_total, p.status)) return it;
-      it.s = static_cast<const T*>(t.src) + so + e;
-      it.d = static_cast<T*>(t.dst) + d_at;
-    } else {
-      x -= nr * per_head;
-      const int hh = x / per_v, c = x - hh * per_v, hd = max(h0, hv) + hh - hv;
-      if (pl.v_dst < 0) return it;
-      const int64_t d_at = pl.v_dst + hd * p.v.dh + c * VW;
-      if (!EXTKV_IN(d_at, VW, p.k_total, p.status)) return it;
-      it.s = static_cast<const T*>(p.v.src) + pl.v_src + hd * p.v.sh + c * VW;
-      it.d = static_cast<T*>(p.v.dst) + d_at;
-    }
-    return it;
-  };
-
   using V = Vec<T, VW>;
-  for (int i0 = tid; i0 < total; i0 += kThreads * kUnroll) {
-    Item it[kUnroll];
-    V a[kUnroll], b[kUnroll];
+
+  // q and k.  A thread keeps one place in the head (a pair of vectors to turn,
+  // or a vector to copy) and walks over the CTA's (row, head)s, kUnroll at a time.
+  const int rot = INTER && VW > 1 ? p.R / VW : half / VW;  // places that turn (single elements: R/2 pairs)
+  const int per_head = rot + (p.D - p.R) / VW;
+  const int nr = max(0, min(h1, hv) - h0);
+  const SmallDiv by_nr(nr);
+  for (int c0 = 0; c0 < per_head; c0 += kThreads) {  // once, but for single elements of wide heads
+    const int here = min(per_head - c0, kThreads), step = kThreads / here;
+    const int lane_h = tid / here, c = c0 + tid - lane_h * here;
+    const int total = lane_h < step ? rows * nr : 0;
+    const bool turn = c < rot;
+    const int e = !turn ? p.R + (c - rot) * VW : INTER && VW == 1 ? 2 * c : c * VW;  // first element
+    const int part = turn && !(INTER && VW > 1) ? (INTER ? 1 : half) : 0;           // distance of the pair's other vector
+    for (int x0 = lane_h; x0 < total; x0 += step * kUnroll) {
+      const T* src[kUnroll];
+      T* dst[kUnroll];
+      int row[kUnroll];
+      V a[kUnroll], b[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      const int i = i0 + u * kThreads;
-      it[u] = i < total ? item_at(i) : Item{nullptr, nullptr, 0, -1};
-      if (it[u].s) {
-        a[u] = *reinterpret_cast<const V*>(it[u].s);
-        if (it[u].part) b[u] = *reinterpret_cast<const V*>(it[u].s + it[u].part);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (!it[u].s) continue;
-      if (it[u].cs >= 0) {
-        if (INTER && VW > 1) {
-          float f[VW];
-          unpack<T, VW>(a[u], f);
-#pragma unroll
-          for (int e = 0; e + 1 < VW; e += 2) {
-            const float2 w = cs[it[u].cs + e / 2];
-            const float x = f[e], y = f[e + 1];
-            f[e] = x * w.x - y * w.y;
-            f[e + 1] = y * w.x + x * w.y;
+      for (int u = 0; u < kUnroll; ++u) {
+        const int x = x0 + u * step;
+        src[u] = nullptr;
+        if (x < total) {
+          const int r = by_nr(x), h = h0 + x - r * nr;
+          const bool is_q = h < p.q.heads;
+          const Tensor& t = is_q ? p.q : p.k;
+          const int hd = is_q ? h : h - p.q.heads;
+          const int64_t to = is_q ? place[r].q_dst : place[r].k_dst;
+          const int64_t d_at = to + hd * t.dh + e;
+          if (to >= 0 && EXTKV_IN(d_at, part + VW, is_q ? p.q_total : p.k_total, p.status)) {
+            src[u] = static_cast<const T*>(t.src) + (is_q ? place[r].q_src : place[r].k_src) + hd * t.sh + e;
+            dst[u] = static_cast<T*>(t.dst) + d_at;
+            row[u] = r;
+            a[u] = *reinterpret_cast<const V*>(src[u]);
+            if (part) b[u] = *reinterpret_cast<const V*>(src[u] + part);
           }
-          pack<T, VW>(a[u], f);
-        } else {
-          float f[VW], g[VW];
-          unpack<T, VW>(a[u], f);
-          unpack<T, VW>(b[u], g);
-#pragma unroll
-          for (int e = 0; e < VW; ++e) {
-            const float2 w = cs[it[u].cs + e];
-            const float x = f[e], y = g[e];
-            f[e] = x * w.x - y * w.y;
-            g[e] = y * w.x + x * w.y;
-          }
-          pack<T, VW>(a[u], f);
-          pack<T, VW>(b[u], g);
         }
       }
-      *reinterpret_cast<V*>(it[u].d) = a[u];
-      if (it[u].part) *reinterpret_cast<V*>(it[u].d + it[u].part) = b[u];
+#pragma unroll
+      for (int u = 0; u < kUnroll; ++u) {
+        if (!src[u]) continue;
+        if (turn) {
+          const float2* w = cs + row[u] * half + c;
+          float f[VW], g[VW];
+          unpack<T, VW>(a[u], f);
+          if (INTER && VW > 1) {
+#pragma unroll
+            for (int i = 0; i + 1 < VW; i += 2) {
+              const float2 q = w[(i / 2) * n_vec];
+              const float x = f[i], y = f[i + 1];
+              f[i] = x * q.x - y * q.y;
+              f[i + 1] = y * q.x + x * q.y;
+            }
+          } else {
+            unpack<T, VW>(b[u], g);
+#pragma unroll
+            for (int i = 0; i < VW; ++i) {
+              const float2 q = w[i * n_vec];
+              const float x = f[i], y = g[i];
+              f[i] = x * q.x - y * q.y;
+              g[i] = y * q.x + x * q.y;
+            }
+            pack<T, VW>(b[u], g);
+          }
+          pack<T, VW>(a[u], f);
+        }
+        *reinterpret_cast<V*>(dst[u]) = a[u];
+        if (part) *reinterpret_cast<V*>(dst[u] + part) = b[u];
+      }
     }
+  }
+
+  // v: copies of whole heads, 16 bytes at a time (D is whole vectors)
+  constexpr int CW = 16 / sizeof(T);
+  const int nv = max(0, h1 - max(h0, hv)), hv0 = max(h0, hv) - hv, per_v = p.D / CW;
+  const int step = kThreads / per_v, lane_h = tid / per_v, e = (tid - lane_h * per_v) * CW;
+  const int total = lane_h < step ? rows * nv : 0;
+  const SmallDiv by_nv(nv);
+  for (int x0 = lane_h; x0 < total; x0 += step * kUnroll) {
+    uint4 a[kUnroll];
+    T* dst[kUnroll];
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u) {
+      const int x = x0 + u * step;
+      dst[u] = nullptr;
+      if (x < total) {
+        const int r = by_nv(x), hd = hv0 + x - r * nv;
+        const int64_t d_at = place[r].v_dst + hd * p.v.dh + e;
+        if (place[r].v_dst >= 0 && EXTKV_IN(d_at, CW, p.k_total, p.status)) {
+          dst[u] = static_cast<T*>(p.v.dst) + d_at;
+          a[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v.src) + place[r].v_src + hd * p.v.sh + e);
+        }
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < kUnroll; ++u)
+      if (dst[u]) *reinterpret_cast<uint4*>(dst[u]) = a[u];
   }
 }
 
@@ -367,12 +384,12 @@ cudaError_t launch_rotary(const RotaryArgs& a) {
   p.status = a.status;
   // Few rows: a CTA per row and per some of its heads, so that a decode step's
   // few hundred kilobytes spread over the GPU (each CTA computes its row's
-  // angles again); many rows: several rows per CTA, which share the loop.
+  // angles again); many rows: as many rows a CTA as make one wave of CTAs.
   const int heads = a.q.heads + a.k.heads + a.v.heads;
-  const int64_t ctas = int64_t(num_sms()) * 4;
+  const int64_t ctas = int64_t(num_sms()) * kMinCtas;
   int hpc = heads;
   while (hpc > 4 && p.n_rows * ((heads + hpc - 1) / hpc) < ctas) hpc = (hpc + 1) / 2;
-  int64_t rpc = hpc == heads ? std::max<int64_t>(1, std::min<int64_t>(kMaxRows, p.n_rows / ctas)) : 1;
+  const int64_t rpc = hpc == heads ? std::min<int64_t>(kMaxRows, (p.n_rows + ctas - 1) / ctas) : 1;
   const int64_t gx = (p.n_rows + rpc - 1) / rpc;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   p.rows_per_cta = static_cast<int>(rpc);
