@@ -49,6 +49,7 @@ struct PagedDecodeArgs {
   void* workspace;
   int32_t* status;
   cudaStream_t stream;
+  uint32_t wait_limit_plus1;  // as AttnArgs
 };
 size_t paged_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype);
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, const char** name);

@@ -228,7 +228,8 @@ int attention_paged_decode(void* y, const void* q, const void* k_pages, const vo
     return fail(EXTKV_ERR_INVALID_ARG, "%s: tensors must be 16-byte aligned", who);
   if (int rc = check_workspace(who, workspace, ws_bytes, paged_decode_workspace_bytes(B, Hq, Hkv, D, dtype))) return rc;
   PagedDecodeArgs a{y,      q,         k_pages,   v_pages,  page_table, nonpad,    scale,  window, B, Hq, Hkv, D,
-                    num_pages, page_size, max_pages, q_stride, dtype,      workspace, status, static_cast<cudaStream_t>(stream)};
+                    num_pages, page_size, max_pages, q_stride, dtype,      workspace, status, static_cast<cudaStream_t>(stream),
+                    wait_limit_setting()};
   const char* name = "";
   note_launches(0);
   const cudaError_t e = launch_paged_decode(a, &name);

@@ -5,16 +5,19 @@
 // bf16), for 4 D (Hq/Hkv) flops.
 //
 // The batch's work is one axis of tiles (KT keys of one unit; a unit is a
-// (sequence, KV head, group of query heads)), unit after unit, and every warp
-// of the GPU takes an equal contiguous slice of it, whatever the sequences'
-// lengths are: a warp streams its slice through its own ring of shared-memory
-// stages (16-byte cp.async, a row's address from the page table, rows outside
-// the sequence filled with zeros), so warps never wait for each other and a
-// page may end anywhere in a tile.  A unit that lies in one slice is written
-// out by its warp; of a unit split over slices each warp leaves (max, sum,
-// unnormalised output) in the workspace, and the merge kernel joins them in
-// slice order, so the result does not depend on timing.
+// (sequence, KV head, group of query heads)), unit after unit.  Every CTA takes
+// an equal contiguous slice of it and every warp an equal part of that,
+// whatever the sequences' lengths are: a warp streams its part through its own
+// ring of shared-memory stages (16-byte cp.async, a row's address from the page
+// table, rows outside the sequence filled with zeros), so warps do not wait for
+// each other while they stream, and a page may end anywhere in a tile.  A unit
+// that lies in one warp's part is written out by it; a unit split over warps of
+// a CTA is joined by the CTA at its end, and one split over CTAs by the merge
+// kernel, from each CTA's (max, sum, unnormalised output) in the workspace.
+// Everything is joined in the order of the axis, so the result does not depend
+// on timing.
 #include <algorithm>
+#include <cstring>
 
 #include "common.cuh"
 #include "internal.h"
@@ -27,6 +30,8 @@ namespace extkv {
 
 namespace {
 
+constexpr uint32_t kWaitPolls = 1u << 22;  // bounded waits
+
 struct PagedParams {
   void* y;
   const void* q;
@@ -37,13 +42,17 @@ struct PagedParams {
   float c;  // scale * log2(e)
   int window, B, Hq, Hkv, g, D, page_size, max_pages;
   int64_t num_pages, q_stride;
+  int box;     // rows of a TMA request
+  uint32_t wait_limit;
   int rows;    // query heads per unit (the kernel's row capacity)
   int groups;  // units per (sequence, KV head)
   int units;   // groups * Hkv: units of a sequence
-  int slices;
+  int slices;     // pieces the axis is cut into that the merge kernel joins: CTAs (tensor cores) or warps
   int64_t* base;  // [B + 1] tiles before each sequence (per unit of it)
   float2* ml;     // [slices][2][rows] (max in log2 units, sum)
   float* part;    // [slices][2][rows][D]
+  float2* w_ml;   // [slices][warps][rows]: partials a CTA joins itself
+  float* w_part;  // [slices][warps][rows][D]
   int32_t* status;
 };
 
@@ -58,21 +67,41 @@ __device__ __forceinline__ LiveKeys live_keys(const PagedParams& p, int b) {
   return {p.window > 0 && n > p.window ? n - p.window : 0, n};
 }
 
+// Tiles start at multiples of KT.
 template <int KT>
 __device__ __forceinline__ int tiles_of(LiveKeys k) {
-  return (k.hi - k.lo + KT - 1) / KT;
+  return k.lo < k.hi ? (k.hi + KT - 1) / KT - k.lo / KT : 0;
 }
 
-// Slices the axis is cut into: one per warp, or one per tile when there are fewer.
-__device__ __forceinline__ int live_slices(const PagedParams& p, int64_t total) {
-  return total < p.slices ? static_cast<int>(total) : p.slices;
-}
+// The axis of tiles cut into slices: p.slices, or one per tile when there are
+// fewer; the first `more` of them hold one tile more than the others.
+struct Axis {
+  int64_t total, each;
+  int n, more;
+  __device__ __forceinline__ Axis(const PagedParams& p, int64_t total_) : total(total_) {
+    n = total < p.slices ? static_cast<int>(total) : p.slices;
+    each = n ? div(total, n) : 0;
+    more = static_cast<int>(total - each * n);
+  }
+  __device__ __forceinline__ int64_t start(int i) const { return i * each + min(i, more); }
+  // the slice that holds tile f
+  __device__ __forceinline__ int holds(int64_t f) const {
+    const int64_t cut = more * (each + 1);
+    return static_cast<int>(f < cut ? div(f, each + 1) : more + div(f - cut, each));
+  }
+  // 64-bit division costs some hundred instructions: not where 32 bits do
+  static __device__ __forceinline__ int64_t div(int64_t a, int64_t b) {
+    return ((a | b) >> 32) == 0 ? static_cast<uint32_t>(a) / static_cast<uint32_t>(b) : a / b;
+  }
+};
 
 // A position on the axis of tiles.
 template <int KT>
 struct Cursor {
   int b, u, t, tiles;
   LiveKeys keys;
+  // the tile's first key
+  __device__ __forceinline__ int key0() const { return (keys.lo / KT + t) * KT; }
   __device__ __forceinline__ void next(const PagedParams& p) {
     if (++t < tiles) return;
     t = 0;
@@ -122,18 +151,17 @@ __device__ __forceinline__ int scan_tiles(const PagedParams& p, int64_t* pre, in
   return per;
 }
 
-// The cursor at tile f of the axis (f < total).
+// The cursor at tile f of the axis (f < total); the warp's lanes search together.
 template <int KT>
 __device__ __forceinline__ Cursor<KT> cursor_at(const PagedParams& p, const int64_t* pre, int per, int64_t f) {
-  int lo = 0, hi = blockDim.x;  // the last chunk whose first tile is <= f
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] * p.units <= f) lo = mid;
-    else hi = mid;
-  }
-  int64_t rest = f - pre[lo] * p.units;
+  // the last chunk of sequences whose first tile is <= f: 32 candidates at a time
+  const int lane = threadIdx.x & 31, chunks = blockDim.x, step = (chunks + 31) / 32;
+  const int wide = __popc(__ballot_sync(0xffffffffu, lane * step < chunks && pre[lane * step] * p.units <= f)) - 1;
+  const int at = wide * step + lane;
+  const int chunk = wide * step + __popc(__ballot_sync(0xffffffffu, lane < step && at < chunks && pre[at] * p.units <= f)) - 1;
+  int64_t rest = f - pre[chunk] * p.units;
   Cursor<KT> c;
-  c.b = lo * per;
+  c.b = chunk * per;
   for (;;) {
     c.keys = live_keys(p, c.b);
     c.tiles = tiles_of<KT>(c.keys);
@@ -142,7 +170,7 @@ __device__ __forceinline__ Cursor<KT> cursor_at(const PagedParams& p, const int6
     rest -= n;
     ++c.b;
   }
-  c.u = static_cast<int>(rest / c.tiles);
+  c.u = static_cast<int>(Axis::div(rest, c.tiles));
   c.t = static_cast<int>(rest - static_cast<int64_t>(c.u) * c.tiles);
   return c;
 }
@@ -155,8 +183,8 @@ struct TileRows {
   bool live;
   __device__ __forceinline__ void look_up(const PagedParams& p, const Cursor<KT>& c) {
     const int lane = threadIdx.x & 31;
-    const int j = c.keys.lo + c.t * KT + lane;
-    live = lane < KT && j < c.keys.hi;
+    const int j = c.key0() + lane;
+    live = lane < KT && j >= c.keys.lo && j < c.keys.hi;
     u = c.u;
     off = 0;
     page = -1;
@@ -194,251 +222,575 @@ __device__ __forceinline__ void cp_async_wait() {
 // maximum and sum are per column.  The path is bound by HBM: its products need
 // about 8 flops a byte, a few percent of the tensor pipe, and tcgen05's 128 rows
 // would be mostly padding.
+//
+// A consumer warp has a ring of slots that hold K and V tiles in turn (KT keys
+// each, 64-column chunks of 128-byte swizzled rows), so that a slot is refilled
+// as soon as its one product is done.  Two ways to fill it:
+//   TMA   pages of whole boxes (page_size a multiple of 16): a producer warp,
+//         one lane per consumer, issues one request for a box of 16 or KT rows.
+//         The consumers then execute no load instructions, which matters: with
+//         three warps an SM at head size 512 a tile's instructions take longer
+//         than its bytes (cp.async by the consumers: 85 us on the 32-sequence
+//         case, its bytes 69 us).
+//   else  any other page size: the consumer's lanes copy 16 bytes each
+//         (cp.async), a row's address from the page table.
 
-template <int D_, int NT_, int KT_, int STAGES_, int WARPS_>
+template <int D_, int NT_, int KT_, int SLOTS_, int WARPS_, bool TMA_>
 struct MmaCfg {
-  static constexpr int D = D_, NT = NT_, KT = KT_, STAGES = STAGES_, WARPS = WARPS_;
-  static constexpr int kRowBytes = D * 2;
-  static constexpr int kTile = KT * kRowBytes;  // one of K, V
-  static constexpr int kStage = 2 * kTile;
-  static constexpr int kSmem = WARPS * STAGES * kStage;
+  static constexpr int D = D_, NT = NT_, KT = KT_, SLOTS = SLOTS_, WARPS = WARPS_;
+  static constexpr bool TMA = TMA_;
+  static constexpr int kThreads = (WARPS + (TMA ? 1 : 0)) * 32;
+  static constexpr int kTile = KT * D * 2;  // a slot
+  static constexpr int kRing = SLOTS * kTile;
+  static constexpr int kSmem = WARPS * kRing + 1024;
 };
 
+// What a warp leaves to its CTA: the units its part begins [0] and ends [1] in,
+// whether the first was left early (to the workspace) and the last late (in the
+// ring), and whether the late one begins and ends its unit.
+struct Rec {
+  int n, early, late, begins, ends;
+  int b[2], u[2];
+};
+
+// Partials of one unit in a CTA: late ones of the warps in `members`, then the
+// early one of warp `early` (-1: none).
+struct Chain {
+  unsigned members;
+  int early, b, u, whole, slot;
+};
+
+// Bounded wait: polls first (the warp has its scheduler almost to itself), then
+// suspends; gives up once another warp has.
+__device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  uint32_t i = 0;
+  for (; i < limit && i < 64; ++i)
+    if (ptx::mbar_test_wait(bar, parity)) return true;
+  for (; i < limit; ++i) {
+    if (ptx::mbar_try_wait(bar, parity)) return true;
+    if ((i & 127u) == 127u && *abort) return false;
+  }
+  *abort = 1;
+  return false;
+}
+
+// Bits of the keys [lo, hi) in a tile of KT keys that starts at k0.
+template <int KT>
+__device__ __forceinline__ uint32_t key_bits(int lo, int hi, int k0) {
+  const int a = max(lo - k0, 0), b = min(hi - k0, KT);
+  if (a >= b) return 0;
+  return (b >= 32 ? ~0u : (1u << b) - 1u) & (~0u << a);
+}
+
 template <class C>
-__global__ void __launch_bounds__(C::WARPS * 32, 1) paged_decode_mma_kernel(const PagedParams p) {
-  constexpr int D = C::D, NT = C::NT, KT = C::KT, ST = C::STAGES, KS = KT / 16;
+__global__ void __launch_bounds__(C::kThreads, 1)
+    paged_decode_mma_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                            const PagedParams p) {
+  constexpr int D = C::D, NT = C::NT, KT = C::KT, NS = C::SLOTS, KS = KT / 16, W = C::WARPS;
   constexpr int kRowsU = 8 * NT;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ int64_t pre[C::WARPS * 32 + 1], warp_sum[C::WARPS];
-  __shared__ uint32_t live_mask[C::WARPS][ST];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kPad = D + 4;  // rows of a partial in shared memory start in different banks
+  constexpr uint32_t kFull = KT == 32 ? ~0u : (1u << (KT & 31)) - 1u;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  __shared__ int64_t pre[C::kThreads + 1], warp_sum[C::kThreads / 32];
+  __shared__ uint32_t live_mask[W][NS];  // keys of the slot's K tile that were loaded
+  __shared__ Rec rec[W];
+  __shared__ Cursor<KT> start_at[W];
+  __shared__ Chain chains[W + 1];
+  __shared__ int n_chains;
+  __shared__ uint64_t full[W][NS], empty[W][NS];
+  __shared__ int abort_flag;
+  volatile int* abort = &abort_flag;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quad = lane >> 2, qi = lane & 3;
+  if (C::TMA) {
+    for (int i = tid; i < W * NS; i += C::kThreads) {
+      ptx::mbar_init(&full[i / NS][i % NS], 1);
+      ptx::mbar_init(&empty[i / NS][i % NS], 1);
+    }
+    if (tid == 0) {
+      abort_flag = 0;
+      ptx::prefetch_tensormap(&kmap);
+      ptx::prefetch_tensormap(&vmap);
+    }
+    ptx::fence_mbar_init();
+  }
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
-  const int per = scan_tiles<KT>(p, pre, warp_sum);
-  const int64_t total = pre[blockDim.x] * p.units;
-  const int slice = warp * gridDim.x + blockIdx.x;  // few tiles: one warp per SM first
-  const int slices = live_slices(p, total);
-  if (slice >= slices) return;
-  const int64_t f0 = total * slice / slices, f1 = total * (slice + 1) / slices;
-  const int n = static_cast<int>(f1 - f0);  // at least one
-
-  const uint32_t ring = ptx::smem_u32(smem) + warp * ST * C::kStage;
-  Cursor<KT> ld = cursor_at<KT>(p, pre, per, f0);
-  Cursor<KT> cur = ld;
-  TileRows<KT> rows;
-  rows.look_up(p, ld);
-  const uint8_t* kp = static_cast<const uint8_t*>(p.k);
-  const uint8_t* vp = static_cast<const uint8_t*>(p.v);
-
-  int issued = 0;
-  auto issue = [&]() {
-    const int s = issued % ST;
-    const uint32_t row = rows.row(p);
-    const uint32_t mask = __ballot_sync(0xffffffffu, row != ~0u);
-    if (lane == 0) live_mask[warp][s] = mask;
-    const uint32_t kd = ring + s * C::kStage, vd = kd + C::kTile;
-    constexpr int kChunks = D / 8;  // 16-byte pieces of a row
-#pragma unroll
-    for (int i = 0; i < KT * kChunks / 32; ++i) {
-      const int x = i * 32 + lane, r = x / kChunks, ch = x % kChunks;
-      const uint32_t pr = __shfl_sync(0xffffffffu, row, r);
-      const uint32_t bytes = pr != ~0u ? 16 : 0;
-      const int64_t at = (pr != ~0u ? static_cast<int64_t>(pr) * C::kRowBytes : 0) + ch * 16;
-      const uint32_t to = r * C::kRowBytes + ((ch ^ (r & 7)) << 4);
-      cp_async_16(kd + to, kp + at, bytes);
-      cp_async_16(vd + to, vp + at, bytes);
-    }
-    ++issued;
-    if (issued < n) {
-      ld.next(p);
-      rows.look_up(p, ld);
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) {
-    if (s < n) issue();
-    cp_async_commit();
+  const int per = scan_tiles<KT>(p, pre, warp_sum);  // meets the whole block
+  const Axis axis(p, pre[blockDim.x] * p.units);
+  const int cta = blockIdx.x;
+  if (cta >= axis.n) return;
+  const int64_t c0 = axis.start(cta);
+  const int tiles_here = static_cast<int>(axis.start(cta + 1) - c0);  // at least one
+  const int mine = C::TMA && warp == W ? min(lane, W - 1) : warp;     // the producer's lanes serve a warp each
+  const int i0 = static_cast<int>(static_cast<int64_t>(tiles_here) * mine / W);
+  const int n = static_cast<int>(static_cast<int64_t>(tiles_here) * (mine + 1) / W) - i0;
+  Cursor<KT> cur{};
+  if (warp < W && n > 0) cur = cursor_at<KT>(p, pre, per, c0 + i0);
+  if constexpr (C::TMA) {
+    if (warp < W && lane == 0) start_at[warp] = cur;
+    __syncthreads();
+    if (warp == W) cur = start_at[mine];
   }
 
-  uint32_t qf[NT][D / 16][2];
-  float o[D / 16][NT][4];
-  float m[NT][2], l[NT][2];
-  bool open = false;  // the unit's first tile of this slice has been taken
-  int t_first = 0, slot = 0;
-  for (int it = 0; it < n; ++it) {
-    if (!open) {
-      open = true;
-      t_first = cur.t;
-      const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
+  if (C::TMA && warp == W) {
+    // ---------------- producer ----------------
+    uint8_t* ring = smem + mine * C::kRing;
+    const int boxes = KT / p.box;  // per tile: 1, or 2
+    int64_t page[2];
+    int off[2];
+    auto look_up = [&] {  // the tile's pages; -2: not needed
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        const int hr = gr * kRowsU + nt * 8 + quad;  // head within the KV head's group
-        const bool in = hr < p.g;
-        const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-            static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + hr) * D);
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          qf[nt][kk][0] = in ? qr[kk * 8 + qi] : 0u;
-          qf[nt][kk][1] = in ? qr[kk * 8 + 4 + qi] : 0u;
-        }
-        m[nt][0] = m[nt][1] = -INFINITY;
-        l[nt][0] = l[nt][1] = 0.f;
+      for (int x = 0; x < 2; ++x) {
+        const int j = cur.key0() + x * p.box, pg = j / p.page_size;
+        off[x] = j - pg * p.page_size;
+        page[x] = -2;
+        if (x < boxes && j < cur.keys.hi && j + p.box > cur.keys.lo)
+          page[x] = p.table[static_cast<int64_t>(cur.b) * p.max_pages + pg];
       }
+    };
+    const int groups = lane < W ? 2 * n : 0;  // K, V, K, V, ...
+    if (groups) look_up();
+    int g = 0, slot = 0, phase = 1;  // phase: of the empty barrier to wait for (none in the first round)
+    uint32_t idle = 0;
+    while (__any_sync(0xffffffffu, g < groups)) {
+      const bool can = g < groups && (g < NS || ptx::mbar_test_wait(&empty[mine][slot], phase));
+      if (can) {
+        const CUtensorMap* map = (g & 1) ? &vmap : &kmap;
+        uint8_t* dst = ring + slot * C::kTile;
+        uint32_t mask = 0, bytes = 0;
+        int row[2];
 #pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt)
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
-    }
-    cp_async_wait<ST - 2>();
-    __syncwarp();  // tile `it` has landed for every lane, and tile it - 1 has been read by every lane
-    const int s = it % ST;
-    const uint32_t mask = live_mask[warp][s];
-    if (issued < n) issue();
-    cp_async_commit();
-    const uint32_t ka = ring + s * C::kStage, va = ka + C::kTile;
-
-    float sc[KS][NT][4];
-#pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) sc[ks][nt][e] = 0.f;
-      const int r = ks * 16 + (lane & 15);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t a0, a1, a2, a3;
-        const int ch = 2 * kk + (lane >> 4);
-        ptx::ldmatrix_x4(a0, a1, a2, a3, ka + r * C::kRowBytes + ((ch ^ (r & 7)) << 4));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(sc[ks][nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
-      }
-    }
-    if (mask != (KT == 32 ? 0xffffffffu : (1u << (KT & 31)) - 1u)) {
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const bool k0 = (mask >> (ks * 16 + quad)) & 1, k1 = (mask >> (ks * 16 + 8 + quad)) & 1;
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          if (!k0) sc[ks][nt][0] = sc[ks][nt][1] = -INFINITY;
-          if (!k1) sc[ks][nt][2] = sc[ks][nt][3] = -INFINITY;
-        }
-      }
-    }
-    float mn[NT][2];
-    bool grow = false;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        float x = -INFINITY;
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) x = fmaxf(x, fmaxf(sc[ks][nt][h], sc[ks][nt][h + 2]));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-        mn[nt][h] = fmaxf(m[nt][h], x);
-        grow |= mn[nt][h] > m[nt][h];
-      }
-    if (__any_sync(0xffffffffu, grow)) {
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float corr = m[nt][h] == -INFINITY ? 0.f : ptx::ex2((m[nt][h] - mn[nt][h]) * p.c);
-          m[nt][h] = mn[nt][h];
-          l[nt][h] *= corr;
-#pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt) {
-            o[mt][nt][h] *= corr;
-            o[mt][nt][h + 2] *= corr;
+        for (int x = 0; x < 2; ++x) {
+          row[x] = -1;
+          if (page[x] == -2) continue;
+          if (page[x] < 0 || page[x] >= p.num_pages) {
+            if (cur.u == 0 && !(g & 1)) report(p.status, EXTKV_DEV_BAD_PAGE);
+            continue;
           }
+          row[x] = static_cast<int>(page[x] * p.Hkv + cur.u / p.groups);
+          bytes += p.box * D * 2;
+          mask |= (p.box == 32 ? ~0u : (1u << p.box) - 1u) << (x * p.box);
         }
-    }
-    uint32_t pb[KS][NT][2];
+        live_mask[mine][slot] = mask;
+        if (bytes) {
+          ptx::mbar_arrive_expect_tx(&full[mine][slot], bytes);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      const float mc0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] * p.c;
-      const float mc1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] * p.c;
-#pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const float e0 = ptx::ex2(fmaf(sc[ks][nt][0], p.c, -mc0)), e1 = ptx::ex2(fmaf(sc[ks][nt][1], p.c, -mc1));
-        const float e2 = ptx::ex2(fmaf(sc[ks][nt][2], p.c, -mc0)), e3 = ptx::ex2(fmaf(sc[ks][nt][3], p.c, -mc1));
-        l[nt][0] += e0 + e2;
-        l[nt][1] += e1 + e3;
-        // P rounded to bf16 for the product (off by at most 2^-8 of each weight; the sum keeps fp32)
-        pb[ks][nt][0] = ptx::movmatrix_trans(ptx::pack_bf16x2(e0, e1));
-        pb[ks][nt][1] = ptx::movmatrix_trans(ptx::pack_bf16x2(e2, e3));
+          for (int x = 0; x < 2; ++x)
+            if (row[x] >= 0) {
+              // chunk by chunk where the box is half a tile: a box lands its chunks one after another
+              if (p.box == KT) {
+                ptx::tma_load_4d(dst, map, &full[mine][slot], 0, off[x], row[x], 0);
+              } else {
+#pragma unroll 1
+                for (int ch = 0; ch < D / 64; ++ch)
+                  ptx::tma_load_4d(dst + ch * (KT * 128) + x * (p.box * 128), map, &full[mine][slot], 0, off[x], row[x], ch);
+              }
+            }
+        } else {
+          ptx::mbar_arrive(&full[mine][slot]);
+        }
+        ++g;
+        if (!(g & 1) && g < groups) {
+          cur.next(p);
+          look_up();
+        }
+        if (++slot == NS) {
+          slot = 0;
+          phase ^= 1;
+        }
       }
+      idle = __any_sync(0xffffffffu, can) ? 0 : idle + 1;
+      if (idle > p.wait_limit) *abort = 1;
+      if (*abort) break;
     }
+    if (*abort) {  // copies still in flight land before the CTA leaves
+      for (int x = g > NS ? g - NS : 0; x < g; ++x) ptx::mbar_wait_bounded(&full[mine][x % NS], (x / NS) & 1, kWaitPolls >> 6);
+    }
+    __syncwarp();
+  } else {
+    // ---------------- consumers ----------------
+    if (lane == 0) rec[warp] = Rec{};
+    const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
+    // place of 16-byte piece ch of row r in a slot
+    auto piece = [](int r, int ch) { return static_cast<uint32_t>((ch >> 3) * (KT * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)); };
+    // cp.async: K, V, K, V, ... of the part's tiles; the page ids are loaded a tile ahead
+    Cursor<KT> ld = cur;
+    TileRows<KT> rows;
+    uint32_t row = ~0u;
+    int issued = 0;
+    if (!C::TMA && n > 0) rows.look_up(p, ld);
+    auto issue = [&]() {
+      if (C::TMA || issued >= 2 * n) return;
+      const bool is_v = issued & 1;
+      const int s = issued % NS;
+      if (!is_v) {
+        row = rows.row(p);
+        const uint32_t mask = __ballot_sync(0xffffffffu, row != ~0u);
+        if (lane == 0) live_mask[warp][s] = mask;
+      }
+      const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v : p.k);
+      constexpr int kChunks = D / 8;  // 16-byte pieces of a row
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const int r = ks * 16 + (lane & 7) + ((lane >> 4) << 3);
-#pragma unroll
-      for (int mt = 0; mt < D / 16; ++mt) {
-        uint32_t a0, a1, a2, a3;
-        const int ch = 2 * mt + ((lane >> 3) & 1);
-        ptx::ldmatrix_x4_trans(a0, a1, a2, a3, va + r * C::kRowBytes + ((ch ^ (r & 7)) << 4));
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(o[mt][nt], a0, a1, a2, a3, pb[ks][nt][0], pb[ks][nt][1]);
+      for (int i = 0; i < KT * kChunks / 32; ++i) {
+        const int x = i * 32 + lane, r = x / kChunks, ch = x % kChunks;
+        const uint32_t pr = __shfl_sync(0xffffffffu, row, r);
+        const int64_t at = (pr != ~0u ? static_cast<int64_t>(pr) * (D * 2) : 0) + ch * 16;
+        cp_async_16(ring + s * C::kTile + piece(r, ch), src + at, pr != ~0u ? 16 : 0);  // no row: zeros
+      }
+      ++issued;
+      if (is_v && issued < 2 * n) {
+        ld.next(p);
+        rows.look_up(p, ld);
+      }
+    };
+    if (!C::TMA) {
+      for (int s = 0; s < NS - 1; ++s) {
+        issue();
+        cp_async_commit();
       }
     }
 
-    const bool unit_end = cur.t == cur.tiles - 1;
-    if (unit_end || it == n - 1) {
-      const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
-      const int heads = min(kRowsU, p.g - gr * kRowsU);
+    uint32_t qf[NT][D / 16][2];
+    float o[D / 16][NT][4];
+    float m[NT][2], l[NT][2];
+    static_assert(kRowsU * (kPad * 4 + 8) <= C::kRing, "a partial fits a warp's ring");
+    int heads = 0;
+    // (max in log2 units, sum) and the unnormalised rows of this warp's unit
+    auto leave = [&](float2* ml, float* part, int stride) {
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-          l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 4);
-          l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 8);
-          l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 16);
-        }
-      if (unit_end && t_first == 0) {
-        __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) +
-                           (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+          const int hr = nt * 8 + qi * 2 + h;
+          if (hr < heads) {
+            if (quad == 0) ml[hr] = make_float2(m[nt][h] * p.c, l[nt][h]);
+            float* dst = part + hr * stride;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
-          const int hr = nt * 8 + quad;
-#pragma unroll
-          for (int mt = 0; mt < D / 16; ++mt) {
-            const uint32_t x = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][0] * i0, o[mt][nt][1] * i1));
-            const uint32_t z = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][2] * i0, o[mt][nt][3] * i1));
-            if (hr < heads) {
-              uint32_t* yr = reinterpret_cast<uint32_t*>(y + hr * D + mt * 16);
-              yr[qi] = x;
-              yr[4 + qi] = z;
+            for (int mt = 0; mt < D / 16; ++mt) {
+              dst[mt * 16 + quad] = o[mt][nt][h];
+              dst[mt * 16 + 8 + quad] = o[mt][nt][h + 2];
             }
           }
         }
+    };
+    bool open = false;  // the unit's first tile of this warp's part has been taken
+    int t_first = 0;
+    int sk = 0, pk = 0;  // slot of the next tile, and its phase
+    for (int it = 0; it < n; ++it) {
+      if (!open) {
+        open = true;
+        t_first = cur.t;
+        if (it == 0 && lane == 0) {
+          rec[warp].n = n;
+          rec[warp].b[0] = cur.b;
+          rec[warp].u[0] = cur.u;
+        }
+        const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const int hr = gr * kRowsU + nt * 8 + quad;  // head within the KV head's group
+          const bool in = hr < p.g;
+          const uint32_t* qr = reinterpret_cast<const uint32_t*>(
+              static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + hr) * D);
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk) {
+            qf[nt][kk][0] = in ? qr[kk * 8 + qi] : 0u;
+            qf[nt][kk][1] = in ? qr[kk * 8 + 4 + qi] : 0u;
+          }
+          m[nt][0] = m[nt][1] = -INFINITY;
+          l[nt][0] = l[nt][1] = 0.f;
+        }
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[mt][nt][e] = 0.f;
+      }
+      // K has landed
+      if constexpr (C::TMA) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&full[warp][sk], pk, abort, p.wait_limit))) break;
       } else {
-        const int64_t at = (static_cast<int64_t>(slice) * 2 + slot) * kRowsU;
+        cp_async_wait<NS - 2>();
+        __syncwarp();  // for every lane, and V of the tile before has been read by every lane
+      }
+      const uint32_t mask = live_mask[warp][sk] & key_bits<KT>(cur.keys.lo, cur.keys.hi, cur.key0());
+      if constexpr (!C::TMA) {
+        issue();
+        cp_async_commit();
+      }
+      const uint32_t ka = ring + sk * C::kTile;
+      float sc[KS][NT][4];
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[ks][nt][e] = 0.f;
+        const int r = ks * 16 + (lane & 15);
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          uint32_t a0, a1, a2, a3;
+          ptx::ldmatrix_x4(a0, a1, a2, a3, ka + piece(r, 2 * kk + (lane >> 4)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(sc[ks][nt], a0, a1, a2, a3, qf[nt][kk][0], qf[nt][kk][1]);
+        }
+      }
+      if constexpr (C::TMA) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[warp][sk]);
+      }
+      if (++sk == NS) {
+        sk = 0;
+        pk ^= 1;
+      }
+      if (mask != kFull) {
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const bool k0 = (mask >> (ks * 16 + quad)) & 1, k1 = (mask >> (ks * 16 + 8 + quad)) & 1;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            if (!k0) sc[ks][nt][0] = sc[ks][nt][1] = -INFINITY;
+            if (!k1) sc[ks][nt][2] = sc[ks][nt][3] = -INFINITY;
+          }
+        }
+      }
+      float mn[NT][2];
+      bool grow = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          float x = -INFINITY;
+#pragma unroll
+          for (int ks = 0; ks < KS; ++ks) x = fmaxf(x, fmaxf(sc[ks][nt][h], sc[ks][nt][h + 2]));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+          x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+          mn[nt][h] = fmaxf(m[nt][h], x);
+          grow |= mn[nt][h] > m[nt][h];
+        }
+      if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const int hr = nt * 8 + qi * 2 + h;
-            if (hr < heads) {
-              if (quad == 0) p.ml[at + hr] = make_float2(m[nt][h] * p.c, l[nt][h]);
-              float* dst = p.part + (at + hr) * D;
+            const float corr = m[nt][h] == -INFINITY ? 0.f : ptx::ex2((m[nt][h] - mn[nt][h]) * p.c);
+            m[nt][h] = mn[nt][h];
+            l[nt][h] *= corr;
 #pragma unroll
-              for (int mt = 0; mt < D / 16; ++mt) {
-                dst[mt * 16 + quad] = o[mt][nt][h];
-                dst[mt * 16 + 8 + quad] = o[mt][nt][h + 2];
-              }
+            for (int mt = 0; mt < D / 16; ++mt) {
+              o[mt][nt][h] *= corr;
+              o[mt][nt][h + 2] *= corr;
             }
           }
       }
-      slot = 1;  // a later unit of the slice is not its first
-      open = false;
+      uint32_t pb[KS][NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        const float mc0 = m[nt][0] == -INFINITY ? 0.f : m[nt][0] * p.c;
+        const float mc1 = m[nt][1] == -INFINITY ? 0.f : m[nt][1] * p.c;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          const float e0 = ptx::ex2(fmaf(sc[ks][nt][0], p.c, -mc0)), e1 = ptx::ex2(fmaf(sc[ks][nt][1], p.c, -mc1));
+          const float e2 = ptx::ex2(fmaf(sc[ks][nt][2], p.c, -mc0)), e3 = ptx::ex2(fmaf(sc[ks][nt][3], p.c, -mc1));
+          l[nt][0] += e0 + e2;
+          l[nt][1] += e1 + e3;
+          // P rounded to bf16 for the product (off by at most 2^-8 of each weight; the sum keeps fp32)
+          pb[ks][nt][0] = ptx::movmatrix_trans(ptx::pack_bf16x2(e0, e1));
+          pb[ks][nt][1] = ptx::movmatrix_trans(ptx::pack_bf16x2(e2, e3));
+        }
+      }
+      // V has landed
+      if constexpr (C::TMA) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&full[warp][sk], pk, abort, p.wait_limit))) break;
+        if (mask != kFull) {
+          // rows of masked keys, whatever they hold, become zeros: their P is 0, and 0 * NaN would be NaN
+          uint8_t* vt = smem + warp * C::kRing + sk * C::kTile;
+          for (int x = lane; x < KT * (D / 8); x += 32) {
+            const int r = x / (D / 8);
+            if (!((mask >> r) & 1)) *reinterpret_cast<uint4*>(vt + piece(r, x % (D / 8))) = make_uint4(0, 0, 0, 0);
+          }
+          ptx::fence_proxy_async_smem();  // before the slot's next copy
+          __syncwarp();
+        }
+      } else {
+        cp_async_wait<NS - 2>();
+        __syncwarp();  // for every lane, and K of this tile has been read by every lane
+        issue();
+        cp_async_commit();
+      }
+      const uint32_t va = ring + sk * C::kTile;
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        const int r = ks * 16 + (lane & 7) + ((lane >> 4) << 3);
+#pragma unroll
+        for (int mt = 0; mt < D / 16; ++mt) {
+          uint32_t a0, a1, a2, a3;
+          ptx::ldmatrix_x4_trans(a0, a1, a2, a3, va + piece(r, 2 * mt + ((lane >> 3) & 1)));
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) ptx::mma_bf16_16816(o[mt][nt], a0, a1, a2, a3, pb[ks][nt][0], pb[ks][nt][1]);
+        }
+      }
+      if constexpr (C::TMA) {
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&empty[warp][sk]);
+      }
+      if (++sk == NS) {
+        sk = 0;
+        pk ^= 1;
+      }
+
+      const bool unit_end = cur.t == cur.tiles - 1;
+      if (unit_end || it == n - 1) {
+        const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
+        heads = min(kRowsU, p.g - gr * kRowsU);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 4);
+            l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 8);
+            l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 16);
+          }
+        if (unit_end && t_first == 0) {
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) +
+                             (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
+            const int hr = nt * 8 + quad;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+              const uint32_t x = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][0] * i0, o[mt][nt][1] * i1));
+              const uint32_t z = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][2] * i0, o[mt][nt][3] * i1));
+              if (hr < heads) {
+                uint32_t* yr = reinterpret_cast<uint32_t*>(y + hr * D + mt * 16);
+                yr[qi] = x;
+                yr[4 + qi] = z;
+              }
+            }
+          }
+        } else if (it < n - 1) {
+          // the first unit of the part, begun before it: to the workspace, the ring is still streaming
+          const int64_t at = (static_cast<int64_t>(cta) * W + warp) * kRowsU;
+          leave(p.w_ml + at, p.w_part + at * D, D);
+          if (lane == 0) rec[warp].early = 1;
+        } else {
+          // the last unit of the part: into the ring, which has been read
+          if (!C::TMA) cp_async_wait<0>();
+          __syncwarp();
+          float* dst = reinterpret_cast<float*>(smem + warp * C::kRing);
+          leave(reinterpret_cast<float2*>(dst + kRowsU * kPad), dst, kPad);
+          if (lane == 0) {
+            rec[warp].late = 1;
+            rec[warp].begins = t_first == 0;
+            rec[warp].ends = unit_end;
+            rec[warp].b[1] = cur.b;
+            rec[warp].u[1] = cur.u;
+          }
+        }
+        open = false;
+      }
+      cur.next(p);
     }
-    cur.next(p);
+  }
+
+  // ---- the units split over this CTA's warps (and maybe its neighbours)
+  __syncthreads();
+  if (C::TMA && *abort) {  // nothing to join: a part is missing
+    if (tid == 0) report(p.status, EXTKV_DEV_TIMEOUT);
+    return;
+  }
+  if (warp == 0) {
+    // lane k looks at warp k's part; a unit's warps are neighbours, so the
+    // members of a chain are the late partials of its unit and the early one
+    // that ends it, if there is one
+    const Rec r = rec[min(lane, W - 1)];
+    const bool some = lane < W && r.n > 0;
+    const unsigned busy = __ballot_sync(0xffffffffu, some);
+    const int64_t head = static_cast<int64_t>(r.b[0]) * p.units + r.u[0];
+    const int64_t last = static_cast<int64_t>(r.b[1]) * p.units + r.u[1];
+    const unsigned behind = busy & (lane < 31 ? ~0u << (lane + 1) : 0u);
+    const int64_t next_head = __shfl_sync(0xffffffffu, head, behind ? __ffs(behind) - 1 : 0);
+    const bool late = some && r.late, early = some && r.early;
+    const bool ends_late = late && !(behind && next_head == last);
+    const int64_t first = __shfl_sync(0xffffffffu, head, __ffs(busy) - 1);
+    int c = 0;
+    for (int w = 0; w < W; ++w)
+#pragma unroll
+      for (int kind = 0; kind < 2; ++kind) {  // 0: ended by w's early partial, 1: by its late one
+        if (!__shfl_sync(0xffffffffu, kind ? ends_late : early, w)) continue;
+        const int64_t id = __shfl_sync(0xffffffffu, kind ? last : head, w);
+        const unsigned members = __ballot_sync(0xffffffffu, late && last == id);
+        const int k0 = members ? __ffs(members) - 1 : 0;
+        const bool begins = __shfl_sync(0xffffffffu, r.begins, k0) && members;
+        const bool ends = kind ? __shfl_sync(0xffffffffu, r.ends, w) : true;
+        if (lane == 0) {
+          Chain x;
+          x.members = members;
+          x.early = kind ? -1 : w;
+          x.b = static_cast<int>(id / p.units);
+          x.u = static_cast<int>(id - static_cast<int64_t>(x.b) * p.units);
+          x.whole = begins && ends;
+          x.slot = id == first ? 0 : 1;  // where the merge kernel looks: the CTA's first unit, or its last
+          chains[c] = x;
+        }
+        ++c;
+      }
+    if (lane == 0) n_chains = c;
+  }
+  __syncthreads();
+  for (int c = 0; c < n_chains; ++c) {
+    const Chain x = chains[c];
+    const int hk = x.u / p.groups, gr = x.u - hk * p.groups, heads = min(kRowsU, p.g - gr * kRowsU);
+    for (int i = tid; i < heads * (D / 4); i += C::kThreads) {
+      const int r = i / (D / 4), c4 = i - r * (D / 4);
+      // the members' (max, sum) and four columns of their rows, all in flight at once
+      float2 ml[W + 1];
+      float4 v[W + 1];
+#pragma unroll
+      for (int k = 0; k < W; ++k) {
+        const float* src = reinterpret_cast<const float*>(smem + k * C::kRing);
+        const bool in = (x.members >> k) & 1;
+        ml[k] = in ? reinterpret_cast<const float2*>(src + kRowsU * kPad)[r] : make_float2(-INFINITY, 0.f);
+        v[k] = in ? reinterpret_cast<const float4*>(src + r * kPad)[c4] : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      ml[W] = make_float2(-INFINITY, 0.f);
+      v[W] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (x.early >= 0) {
+        const int64_t at = (static_cast<int64_t>(cta) * W + x.early) * kRowsU + r;
+        ml[W] = __ldcg(p.w_ml + at);
+        v[W] = __ldcg(reinterpret_cast<const float4*>(p.w_part + at * D) + c4);
+      }
+      float M = -INFINITY;
+#pragma unroll
+      for (int k = 0; k <= W; ++k) M = fmaxf(M, ml[k].x);
+      const float ref = M == -INFINITY ? 0.f : M;
+      float L = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k <= W; ++k) {
+        const float wt = ml[k].x == -INFINITY ? 0.f : ptx::ex2(ml[k].x - ref);  // -inf: absent, or every key skipped
+        L = fmaf(wt, ml[k].y, L);
+        acc.x = fmaf(wt, v[k].x, acc.x);
+        acc.y = fmaf(wt, v[k].y, acc.y);
+        acc.z = fmaf(wt, v[k].z, acc.z);
+        acc.w = fmaf(wt, v[k].w, acc.w);
+      }
+      if (x.whole) {
+        const float inv = L != 0.f ? 1.f / L : 0.f;
+        uint2* y = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) +
+                                            (static_cast<int64_t>(x.b) * p.Hq + hk * p.g + gr * kRowsU + r) * D);
+        y[c4] = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+      } else {
+        const int64_t at = (static_cast<int64_t>(cta) * 2 + x.slot) * kRowsU + r;
+        if (c4 == 0) p.ml[at] = make_float2(M, L);
+        reinterpret_cast<float4*>(p.part + at * D)[c4] = acc;
+      }
+    }
   }
 }
 
@@ -463,11 +815,10 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   const int per = scan_tiles<KT>(p, pre, warp_sum);
-  const int64_t total = pre[blockDim.x] * p.units;
-  const int slice = warp * gridDim.x + blockIdx.x;
-  const int slices = live_slices(p, total);
-  if (slice >= slices) return;
-  const int64_t f0 = total * slice / slices, f1 = total * (slice + 1) / slices;
+  const Axis axis(p, pre[blockDim.x] * p.units);
+  const int slice = warp * gridDim.x + blockIdx.x;  // few tiles: one warp per SM first
+  if (slice >= axis.n) return;
+  const int64_t f0 = axis.start(slice), f1 = axis.start(slice + 1);
   const int n = static_cast<int>(f1 - f0);  // at least one
 
   const int stride = simt_stride<T>(D);
@@ -607,13 +958,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
     for (int d = tid; d < D; d += kMergeThreads) y[d] = Elem<T>::from_float(0.f);
     return;
   }
-  const int slices = live_slices(p, total);
+  const Axis axis(p, total);
   const int64_t u0 = b0 * p.units + static_cast<int64_t>(hk * p.groups + gr) * tiles;
-  // the slice that holds tile f is the last whose first tile is <= f
-  const int s0 = static_cast<int>(((u0 + 1) * slices - 1) / total);
-  const int s1 = static_cast<int>(((u0 + tiles) * slices - 1) / total);
+  const int s0 = axis.holds(u0), s1 = axis.holds(u0 + tiles - 1);
   if (s0 == s1) return;  // written by the slice itself
-  const int first_slot = total * s0 / slices < u0 ? 1 : 0;
+  const int first_slot = axis.start(s0) < u0 ? 1 : 0;
   const int n = s1 - s0 + 1;
   // partial i of the unit, in rows of the workspace
   auto at = [&](int i) { return (static_cast<int64_t>(s0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.rows + r; };
@@ -690,7 +1039,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
 
 struct Plan {
   int rows, groups, warps, slices;
-  size_t off_ml, off_part, bytes;
+  size_t off_ml, off_part, off_w_ml, off_w_part, bytes;
 };
 
 bool use_mma(int64_t D, int dtype) {
@@ -701,6 +1050,7 @@ bool use_mma(int64_t D, int dtype) {
 // accumulators fit the registers (D/4 a thread and eight heads).
 int unit_rows(int64_t g, int64_t D, bool mma) { return mma && g > 8 && D <= 256 ? 16 : 8; }
 
+// Consumer warps of the tensor-core kernels.
 int mma_warps(int64_t D) { return D <= 128 ? 8 : D == 256 ? 6 : 3; }
 
 Plan plan_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
@@ -710,22 +1060,45 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   pl.rows = unit_rows(g, D, mma);
   pl.groups = static_cast<int>((g + pl.rows - 1) / pl.rows);
   pl.warps = mma ? mma_warps(D) : kSimtWarps;
-  pl.slices = std::min(num_sms() * pl.warps, kMaxSlices / pl.warps * pl.warps);
+  pl.slices = mma ? std::min(num_sms(), kMaxSlices) : std::min(num_sms() * pl.warps, kMaxSlices / pl.warps * pl.warps);
   auto up = [](size_t x) { return (x + 255) & ~size_t(255); };
   pl.off_ml = up(sizeof(int64_t) * (B + 1));
   pl.off_part = pl.off_ml + up(sizeof(float2) * 2 * pl.slices * pl.rows);
-  pl.bytes = pl.off_part + up(sizeof(float) * 2 * pl.slices * pl.rows * D);
+  pl.off_w_ml = pl.off_part + up(sizeof(float) * 2 * pl.slices * pl.rows * D);
+  pl.off_w_part = pl.off_w_ml + (mma ? up(sizeof(float2) * pl.slices * pl.warps * pl.rows) : 0);
+  pl.bytes = pl.off_w_part + (mma ? up(sizeof(float) * pl.slices * pl.warps * pl.rows * D) : 0);
   return pl;
 }
 
 template <class C>
-cudaError_t launch_mma(const PagedParams& p, cudaStream_t s) {
-  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(paged_decode_mma_kernel<C>), C::kSmem);
-      e != cudaSuccess)
-    return e;
-  PdlLaunch l(dim3(p.slices / C::WARPS), C::WARPS * 32, C::kSmem, s);
-  cudaError_t e = cudaLaunchKernelEx(&l.cfg, paged_decode_mma_kernel<C>, p);
+cudaError_t launch_mma_cfg(PagedParams p, cudaStream_t s) {
+  auto k = paged_decode_mma_kernel<C>;
+  CUtensorMap kmap, vmap;
+  std::memset(&kmap, 0, sizeof kmap);
+  std::memset(&vmap, 0, sizeof vmap);
+  if (C::TMA) {
+    // (64 columns, row of a page, page and head, 64-column chunk)
+    p.box = p.page_size % C::KT == 0 ? C::KT : 16;
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(p.page_size), static_cast<uint64_t>(p.num_pages) * p.Hkv, C::D / 64};
+    const uint64_t str[3] = {C::D * 2, static_cast<uint64_t>(p.page_size) * C::D * 2, 128};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(p.box), 1, p.box == C::KT ? C::D / 64 : 1};
+    if (!make_tensor_map_bf16(&kmap, p.k, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
+        !make_tensor_map_bf16(&vmap, p.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
+      return cudaErrorInvalidValue;
+  }
+  if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), C::kSmem); e != cudaSuccess) return e;
+  PdlLaunch l(dim3(p.slices), C::kThreads, C::kSmem, s);
+  cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, kmap, vmap, p);
   return e != cudaSuccess ? e : cudaGetLastError();
+}
+
+template <int D, int NT, int KT, int SLOTS, int WARPS>
+cudaError_t launch_mma(const PagedParams& p, cudaStream_t s) {
+  // A request is a box of 16 rows at least: pages of other sizes take cp.async.
+  // (The strides of a tensor map end at 2^40 bytes.)
+  const bool tma = p.page_size % 16 == 0 && static_cast<int64_t>(p.page_size) * D * 2 < (int64_t(1) << 40);
+  return tma ? launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, true>>(p, s)
+             : launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, false>>(p, s);
 }
 
 template <typename T, int DPL, int KT>
@@ -788,15 +1161,18 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, const char** name) {
   p.base = reinterpret_cast<int64_t*>(ws);
   p.ml = reinterpret_cast<float2*>(ws + pl.off_ml);
   p.part = reinterpret_cast<float*>(ws + pl.off_part);
+  p.w_ml = reinterpret_cast<float2*>(ws + pl.off_w_ml);
+  p.w_part = reinterpret_cast<float*>(ws + pl.off_w_part);
   p.status = a.status;
+  p.wait_limit = wait_limit(a.wait_limit_plus1, kWaitPolls);
   cudaError_t e;
   if (use_mma(a.D, a.dtype)) {
     *name = "paged_decode_mma";
     const bool two = pl.rows == 16;
-    if (a.D == 64) e = two ? launch_mma<MmaCfg<64, 2, 32, 3, 8>>(p, a.stream) : launch_mma<MmaCfg<64, 1, 32, 3, 8>>(p, a.stream);
-    else if (a.D == 128) e = two ? launch_mma<MmaCfg<128, 2, 16, 3, 8>>(p, a.stream) : launch_mma<MmaCfg<128, 1, 16, 3, 8>>(p, a.stream);
-    else if (a.D == 256) e = two ? launch_mma<MmaCfg<256, 2, 16, 2, 6>>(p, a.stream) : launch_mma<MmaCfg<256, 1, 16, 2, 6>>(p, a.stream);
-    else e = launch_mma<MmaCfg<512, 1, 16, 2, 3>>(p, a.stream);
+    if (a.D == 64) e = two ? launch_mma<64, 2, 32, 5, 8>(p, a.stream) : launch_mma<64, 1, 32, 5, 8>(p, a.stream);
+    else if (a.D == 128) e = two ? launch_mma<128, 2, 32, 3, 8>(p, a.stream) : launch_mma<128, 1, 32, 3, 8>(p, a.stream);
+    else if (a.D == 256) e = two ? launch_mma<256, 2, 16, 4, 6>(p, a.stream) : launch_mma<256, 1, 16, 4, 6>(p, a.stream);
+    else e = launch_mma<512, 1, 16, 4, 3>(p, a.stream);
   } else {
     *name = a.dtype == EXTKV_F32 ? "paged_decode_simt_f32" : "paged_decode_simt_bf16";
     e = a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);

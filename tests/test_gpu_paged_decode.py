@@ -272,3 +272,34 @@ def test_other_stream_prepared_and_captured():
     rec.step()
     torch.cuda.synchronize()
     assert torch.equal(out, outs[0][0])
+
+
+@pytest.mark.parametrize("D,keys", [(64, 32), (128, 16), (256, 16), (512, 16)])
+@pytest.mark.parametrize("per_warp", [1, 2, 5])
+def test_one_sequence_over_every_warp(D, keys, per_warp):
+    """Lengths that give every warp of the GPU about per_warp tiles: each CTA joins
+    its warps' partials, the merge kernel the CTAs'."""
+    warps = torch.cuda.get_device_properties(0).multi_processor_count * 8
+    n = warps * keys * per_warp + 3
+    q, k, v, table, nonpad = make((n,), 4, 1, D, 64, torch.bfloat16)
+    y = run(q, k, v, table, nonpad, 1.0 / math.sqrt(D), 0)
+    ref, tol = reference(q, k, v, table, (n,), 0, 1.0 / math.sqrt(D))
+    # the bound grows with the number of keys; the errors of independent roundings do not: hold the
+    # result also to a tenth of one partial's share of the output
+    check(y, ref, tol, "y")
+    assert float((y.double() - ref).norm() / ref.norm()) < 2.0 ** -7
+
+
+def test_a_wait_that_runs_out_is_reported():
+    """A poll limit of zero: the ring's waits give up, the status word says so, and
+    the next call is whole again."""
+    lens = (300, 77, 0, 5000)
+    q, k, v, table, nonpad = make(lens, 4, 2, 128, 16, torch.bfloat16)
+    y = torch.empty_like(q)
+    st = ek.new_status()
+    with ek.wait_polls(0):
+        ek.attention_paged_decode(y, q, k, v, table, nonpad, 0.1, status=st)
+    assert ek.extkv_read_status(st) == ek.EXTKV_ERR_DEVICE and int(st[0]) == ek.EXTKV_DEV_TIMEOUT
+    y = run(q, k, v, table, nonpad, 0.1, 0)
+    ref, tol = reference(q, k, v, table, lens, 0, 0.1)
+    check(y, ref, tol, "after")
