@@ -228,10 +228,9 @@ __device__ __forceinline__ void cp_async_wait() {
 // as soon as its one product is done.  Two ways to fill it:
 //   TMA   pages of whole boxes (page_size a multiple of 16): a producer warp,
 //         one lane per consumer, issues one request for a box of 16 or KT rows.
-//         The consumers then execute no load instructions, which matters: with
-//         three warps an SM at head size 512 a tile's instructions take longer
-//         than its bytes (cp.async by the consumers: 85 us on the 32-sequence
-//         case, its bytes 69 us).
+//         The consumers then execute no load instructions: a few warps a
+//         scheduler hold the whole register file, and a tile's instructions
+//         should take no longer than its bytes.
 //   else  any other page size: the consumer's lanes copy 16 bytes each
 //         (cp.async), a row's address from the page table.
 
@@ -1051,7 +1050,7 @@ bool use_mma(int64_t D, int dtype) {
 int unit_rows(int64_t g, int64_t D, bool mma) { return mma && g > 8 && D <= 256 ? 16 : 8; }
 
 // Consumer warps of the tensor-core kernels.
-int mma_warps(int64_t D) { return D <= 128 ? 8 : D == 256 ? 6 : 3; }
+int mma_warps(int64_t D) { return D == 256 ? 4 : 6; }
 
 Plan plan_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   const bool mma = use_mma(D, dtype);
@@ -1169,10 +1168,10 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, const char** name) {
   if (use_mma(a.D, a.dtype)) {
     *name = "paged_decode_mma";
     const bool two = pl.rows == 16;
-    if (a.D == 64) e = two ? launch_mma<64, 2, 32, 5, 8>(p, a.stream) : launch_mma<64, 1, 32, 5, 8>(p, a.stream);
-    else if (a.D == 128) e = two ? launch_mma<128, 2, 32, 3, 8>(p, a.stream) : launch_mma<128, 1, 32, 3, 8>(p, a.stream);
-    else if (a.D == 256) e = two ? launch_mma<256, 2, 16, 4, 6>(p, a.stream) : launch_mma<256, 1, 16, 4, 6>(p, a.stream);
-    else e = launch_mma<512, 1, 16, 4, 3>(p, a.stream);
+    if (a.D == 64) e = two ? launch_mma<64, 2, 32, 8, 6>(p, a.stream) : launch_mma<64, 1, 32, 8, 6>(p, a.stream);
+    else if (a.D == 128) e = two ? launch_mma<128, 2, 32, 4, 6>(p, a.stream) : launch_mma<128, 1, 32, 4, 6>(p, a.stream);
+    else if (a.D == 256) e = two ? launch_mma<256, 2, 16, 6, 4>(p, a.stream) : launch_mma<256, 1, 16, 6, 4>(p, a.stream);
+    else e = launch_mma<512, 1, 16, 2, 6>(p, a.stream);
   } else {
     *name = a.dtype == EXTKV_F32 ? "paged_decode_simt_f32" : "paged_decode_simt_bf16";
     e = a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);
