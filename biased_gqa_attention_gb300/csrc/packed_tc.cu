@@ -10,14 +10,16 @@
 // scores go through the softmax, the tensor cores work for the other.
 //   warp 0       loads: Q tiles, then K and V tiles of 128 keys through a ring
 //                of shared-memory units (TMA, 128-byte swizzle)
-//   warp 1       issues the MMAs: for each key tile PV_A(j-1), QK_A(j),
-//                PV_B(j-1), QK_B(j); S and O live in tensor memory, P (bf16)
-//                over the first half of its S
+//   warps 1, 2   issue the MMAs of tile A and of tile B: PV(j-1), QK(j) for each
+//                key tile; S and O live in tensor memory, P (bf16) over the
+//                first half of its S.  Issuing a 128 x 128 x 16 MMA costs its
+//                thread longer than the tensor pipe takes for it (64 cycles),
+//                so one thread for both tiles left the pipe idle half the time
 //   warps 4-7    softmax and output of tile A, a query row per thread
 //   warps 8-11   the same for tile B
-// (warps 2 and 3 only fill the first warpgroup, which gives its registers to
-// the other two: 72 against 216 of the 168 a thread the block starts with.)
-// The tensor pipe runs one thread's MMAs in order, so S_t(j) being complete
+// (warp 3 only fills the first warpgroup, which gives its registers to the other
+// two: 72 against 216 of the 168 a thread the block starts with.)
+// The tensor pipe runs a thread's MMAs in order, so S_t(j) being complete
 // implies that PV_t(j-1) is: a softmax warp may rescale O_t before it releases
 // P_t(j) without another barrier.  O is rescaled only when a row's maximum has
 // grown by more than 8 in the exponent (P then stays below 2^8, exact enough in
@@ -53,8 +55,8 @@ struct Cfg {
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t u_full[kMaxUnits], u_empty[kMaxUnits];
-  uint64_t s_full[2], p_full[2], o_full[2], o_free[2];
-  uint64_t v_tail, drain;
+  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // p_full: of each half of P
+  uint64_t v_tail, drain[2];
   uint32_t tmem_base;
   int abort;
 };
@@ -88,16 +90,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_init(&bar.q_full[t], 1);
       ptx::mbar_init(&bar.q_empty[t], 1);
       ptx::mbar_init(&bar.s_full[t], 1);
-      ptx::mbar_init(&bar.p_full[t], 128);
+      ptx::mbar_init(&bar.p_full[t][0], 4);
+      ptx::mbar_init(&bar.p_full[t][1], 4);
       ptx::mbar_init(&bar.o_full[t], 1);
       ptx::mbar_init(&bar.o_free[t], 128);
     }
     for (int u = 0; u < C::kUnits; ++u) {
       ptx::mbar_init(&bar.u_full[u], 1);
-      ptx::mbar_init(&bar.u_empty[u], 1);
+      ptx::mbar_init(&bar.u_empty[u], 2);
     }
     ptx::mbar_init(&bar.v_tail, 1);
-    ptx::mbar_init(&bar.drain, 1);
+    for (int t = 0; t < 2; ++t) ptx::mbar_init(&bar.drain[t], 1);
     bar.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -182,69 +185,68 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
     }
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- MMAs ----------------
+  } else if (warp < 3) {
+    // ---------------- MMAs of one query tile ----------------
     if (lane == 0) {
-      const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
-      const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
-      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kBN * 128, 1024);
-      int u = 0, nq[2] = {0, 0}, np[2] = {0, 0};
+      const int t = warp - 1;
+      const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm + t * C::kTile), 16, 1024);
+      const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
+      const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kBN * 128, 1024);
+      const uint32_t ts = tbase + t * kBN, to = tbase + C::kOCol + t * D;
+      int u = 0, nq = 0, np = 0;
       bool ok = true, issued = false;
-      // P_t(j) V_j; uv: the unit of V_j; first: of the item
-      auto pv = [&](int t, int uv, bool first) -> bool {
-        if (first && nq[t] > 1 && !wait_or_abort(&bar.o_free[t], (nq[t] - 2) & 1, abort, lim)) return false;
-        if (!wait_or_abort(&bar.p_full[t], np[t] & 1, abort, lim)) return false;
-        ++np[t];
-        ptx::tc_fence_after();
-        const uint64_t vd = vdesc0 + (((uv % C::kUnits) * C::kTile) >> 4);
-#pragma unroll
-        for (int k = 0; k < kBN / 16; ++k)
-          ptx::umma_bf16_ts(tbase + C::kOCol + t * D, tbase + t * kBN + k * 8, vd + ((k * 2048) >> 4), C::kIdescPV,
-                            (!first || k > 0) ? 1u : 0u);
-        return true;
-      };
-      auto qk = [&](int t, int uk) {
-        const uint64_t qd = qdesc0 + ((t * C::kTile) >> 4), kd = kdesc0 + (((uk % C::kUnits) * C::kTile) >> 4);
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-          const uint32_t off = ((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4;
-          ptx::umma_bf16(tbase + t * kBN, qd + off, kd + off, C::kIdescQK, k > 0);
-        }
-        ptx::umma_commit(&bar.s_full[t]);
-      };
+      auto landed = [&](int x) { return spin_or_abort(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, abort, lim); };
       Rounds rounds(n_work, blockIdx.x, gridDim.x);
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at(p, wi);
+        const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
         issued = true;
-        for (int t = 0; t < 2; ++t) nq[t] += w.lo[t] < w.hi[t];
-        for (int kt = w.k_lo; kt <= w.k_hi && ok; ++kt) {
-          const int uk = u, uv = u - 1;  // K_kt and V_{kt-1}
-          if (kt < w.k_hi && !(ok = wait_or_abort(&bar.u_full[uk % C::kUnits], (uk / C::kUnits) & 1, abort, lim))) break;
-          if (kt > w.k_lo && !(ok = wait_or_abort(&bar.u_full[uv % C::kUnits], (uv / C::kUnits) & 1, abort, lim))) break;
-          ptx::tc_fence_after();
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (kt - 1 >= w.lo[t] && kt - 1 < w.hi[t]) {
-              if (!(ok = pv(t, uv, kt - 1 == w.lo[t]))) break;
-              if (kt == w.hi[t]) ptx::umma_commit(&bar.o_full[t]);
-            }
-            if (kt >= w.lo[t] && kt < w.hi[t]) {
-              if (kt == w.lo[t] && !(ok = wait_or_abort(&bar.q_full[t], (nq[t] - 1) & 1, abort, lim))) break;
+        nq += lo < hi;
+        for (int kt = w.k_lo; kt <= w.k_hi; ++kt) {
+          // P(kt-1) V(kt-1), then Q K(kt)^T over the S that held P(kt-1); K and V
+          // are waited for first, they are mostly there
+          const bool pv = kt > lo && kt <= hi, qk = kt >= lo && kt < hi;
+          if (!(ok = kt == w.k_lo || landed(u - 1)) || !(ok = kt == w.k_hi || landed(u))) break;
+          if (pv) {
+            const bool first = kt - 1 == lo;
+            if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free[t], (nq - 2) & 1, abort, lim))) break;
+            const uint64_t vd = vdesc + ((((u - 1) % C::kUnits) * C::kTile) >> 4);
+            for (int h = 0; h < 2 && ok; ++h) {  // the first half of the keys while the second goes through the softmax
+              if (!(ok = spin_or_abort(&bar.p_full[t][h], np & 1, abort, lim))) break;
               ptx::tc_fence_after();
-              qk(t, uk);
-              if (kt == w.hi[t] - 1) ptx::umma_commit(&bar.q_empty[t]);
+#pragma unroll
+              for (int k = 0; k < kBN / 32; ++k) {
+                const int ks = h * (kBN / 32) + k;
+                ptx::umma_bf16_ts(to, ts + ks * 8, vd + ((ks * 2048) >> 4), C::kIdescPV, (!first || ks > 0) ? 1u : 0u);
+              }
             }
+            if (!ok) break;
+            ++np;
+            if (kt == hi) ptx::umma_commit(&bar.o_full[t]);
           }
-          if (!ok) break;
-          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[uv % C::kUnits]);
-          if (kt < w.k_hi) ptx::umma_commit(&bar.u_empty[uk % C::kUnits]);
-          u += kt < w.k_hi ? 2 : 0;
+          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[(u - 1) % C::kUnits]);
+          if (qk) {
+            if (kt == lo && !(ok = wait_or_abort(&bar.q_full[t], (nq - 1) & 1, abort, lim))) break;
+            ptx::tc_fence_after();
+            const uint64_t kd = kdesc + (((u % C::kUnits) * C::kTile) >> 4);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k) {
+              const uint32_t off = ((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4;
+              ptx::umma_bf16(ts, qdesc + off, kd + off, C::kIdescQK, k > 0);
+            }
+            ptx::umma_commit(&bar.s_full[t]);
+            if (kt == hi - 1) ptx::umma_commit(&bar.q_empty[t]);
+          }
+          if (kt < w.k_hi) {
+            ptx::umma_commit(&bar.u_empty[u % C::kUnits]);
+            u += 2;
+          }
         }
       }
       // every MMA issued has completed before tensor memory is released
       if (issued) {
-        ptx::umma_commit(&bar.drain);
-        if (!ptx::mbar_wait_bounded(&bar.drain, 0, kWaitPolls)) *abort = 1;
+        ptx::umma_commit(&bar.drain[t]);
+        if (!ptx::mbar_wait_bounded(&bar.drain[t], 0, kWaitPolls)) *abort = 1;
       }
     }
     __syncwarp();
@@ -272,16 +274,17 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int kt = lo; kt < hi; ++kt) {
         const int k0 = kt * kBN;
-        if (!__all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
+        if (!__all_sync(0xffffffffu, spin_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
           ok = false;
           break;
         }
         ++ns;
         ptx::tc_fence_after();
         // PV_t(kt - 1) is complete: S_t(kt) was issued after it
-        softmax_tile<D>(ts, to, ra, rb, k0, c, m, l, [] { return true; });
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&bar.p_full[t]);
+        softmax_tile<D>(ts, to, ra, rb, k0, c, m, l, [] { return true; },
+                        [&](int h) {
+                          if (lane == 0) ptx::mbar_arrive(&bar.p_full[t][h]);
+                        });
       }
       if (!ok) break;
       if (!__all_sync(0xffffffffu, wait_or_abort(&bar.o_full[t], no & 1, abort, lim))) {

@@ -23,6 +23,14 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   return false;
 }
 
+// The same, polling without suspending at first: a poll sees the phase some
+// hundred cycles earlier.
+__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  for (uint32_t i = 0; i < limit && i < 4096; ++i)
+    if (ptx::mbar_test_wait(bar, parity)) return true;
+  return wait_or_abort(bar, parity, abort, limit);
+}
+
 // One entry of the work list for one head group: two query tiles of
 // tile_tok / 2 tokens each.
 struct Work {
@@ -78,10 +86,11 @@ struct Rounds {
 // (D columns) when the maximum has grown by more than kGrow, so that P stays
 // below 2^8.  [ra, rb): the row's keys; k0: the tile's first; c: scale * log2(e).
 // `o_ready` is asked before O is rescaled: the product that last wrote it must
-// be complete (false: that wait gave up, and so does this).
-template <int D, class F>
+// be complete (false: that wait gave up, and so does this).  `release(h)` runs,
+// with the warp together, when half h of P (64 keys) can be read.
+template <int D, class F, class G>
 __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, int ra, int rb, int k0, float c, float& m,
-                                             float& l, F o_ready) {
+                                             float& l, F o_ready, G release) {
   uint32_t s[4][32];
 #pragma unroll
   for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
@@ -141,10 +150,13 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, int ra, i
       pk[x] = ptx::pack_bf16x2(e0, e1);
     }
     ptx::tmem_st32(ts + 32 * hf, pk);
+    ptx::tmem_wait_st();
+    ptx::tc_fence_before();
+    __syncwarp();
+    release(hf);
   }
   const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
   l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
-  ptx::tmem_wait_st();
   return true;
 }
 

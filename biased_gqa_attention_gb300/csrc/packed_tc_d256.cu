@@ -42,7 +42,7 @@ static_assert(kSmem <= 232448, "shared memory");
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t u_full[kUnits], u_empty[kUnits], v_land[kUnits];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2][2], pv_done[2];  // of each S; p_full of each half of its P
   uint64_t o_full, o_free, drain;
   uint32_t tmem_base;
   int abort;
@@ -72,7 +72,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     for (int s = 0; s < 2; ++s) {
       ptx::mbar_init(&bar.s_full[s], 1);
-      ptx::mbar_init(&bar.p_full[s], 128);
+      ptx::mbar_init(&bar.p_full[s][0], 4);
+      ptx::mbar_init(&bar.p_full[s][1], 4);
       ptx::mbar_init(&bar.pv_done[s], 1);
     }
     ptx::mbar_init(&bar.o_full, 1);
@@ -176,7 +177,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       auto qk = [&](bool active, bool first) -> bool {
         for (int part = 0; part < 2; ++part, ++u) {
           const int s = u % kUnits;
-          if (!wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
+          if (!spin_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
           ptx::tc_fence_after();
           if (active) {
             if (first && part == 0) {
@@ -202,12 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       auto pv = [&](bool active, bool first) -> bool {
         for (int part = 0; part < 2; ++part, ++u) {
           const int s = u % kUnits;
-          if (!wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
+          if (!spin_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
           if (active) {
-            if (part == 0) {
-              if (first && nq > 1 && !wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim)) return false;
-              if (!wait_or_abort(&bar.p_full[cp & 1], (cp >> 1) & 1, abort, lim)) return false;
-            }
+            if (part == 0 && first && nq > 1 && !wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim)) return false;
+            if (!spin_or_abort(&bar.p_full[cp & 1][part], (cp >> 1) & 1, abort, lim)) return false;
             ptx::tc_fence_after();
             const uint64_t vd = vdesc0 + ((s * kUnit) >> 4);
 #pragma unroll
@@ -260,17 +259,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (!valid) ra = rb = 0;
       float m = -INFINITY, l = 0.f;
       for (int kt = lo; kt < hi; ++kt, ++n) {
-        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
+        if (!(ok = __all_sync(0xffffffffu, spin_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
         ptx::tc_fence_after();
         ok = softmax_tile<D>(ts + (n & 1) * kBN, to, ra, rb, kt * kBN, p.c, m, l, [&] {
           const bool done =
               __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, lim));
           ptx::tc_fence_after();
           return done;
+        }, [&](int h) {
+          if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][h]);
         });
         if (!ok) break;
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&bar.p_full[n & 1]);
       }
       if (!ok || !(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.o_full, no & 1, abort, lim)))) break;
       ++no;
