@@ -195,7 +195,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const uint32_t ts = tbase + t * kBN, to = tbase + C::kOCol + t * D;
       int u = 0, nq = 0, np = 0;
       bool ok = true, issued = false;
-      auto landed = [&](int x) { return spin_or_abort(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, abort, lim); };
+      auto landed = [&](int x) { return wait_or_abort(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, abort, lim); };
       Rounds rounds(n_work, blockIdx.x, gridDim.x);
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at(p, wi);
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free[t], (nq - 2) & 1, abort, lim))) break;
             const uint64_t vd = vdesc + ((((u - 1) % C::kUnits) * C::kTile) >> 4);
             for (int h = 0; h < 2 && ok; ++h) {  // the first half of the keys while the second goes through the softmax
-              if (!(ok = spin_or_abort(&bar.p_full[t][h], np & 1, abort, lim))) break;
+              if (!(ok = wait_or_abort(&bar.p_full[t][h], np & 1, abort, lim))) break;
               ptx::tc_fence_after();
 #pragma unroll
               for (int k = 0; k < kBN / 32; ++k) {
@@ -224,7 +224,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ++np;
             if (kt == hi) ptx::umma_commit(&bar.o_full[t]);
           }
-          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[(u - 1) % C::kUnits]);
           if (qk) {
             if (kt == lo && !(ok = wait_or_abort(&bar.q_full[t], (nq - 1) & 1, abort, lim))) break;
             ptx::tc_fence_after();
@@ -237,6 +236,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
             ptx::umma_commit(&bar.s_full[t]);
             if (kt == hi - 1) ptx::umma_commit(&bar.q_empty[t]);
           }
+          // the slots' commits behind the products: S is what the softmax waits for
+          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[(u - 1) % C::kUnits]);
           if (kt < w.k_hi) {
             ptx::umma_commit(&bar.u_empty[u % C::kUnits]);
             u += 2;
@@ -274,7 +275,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       float m = -INFINITY, l = 0.f;
       for (int kt = lo; kt < hi; ++kt) {
         const int k0 = kt * kBN;
-        if (!__all_sync(0xffffffffu, spin_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
+        if (!__all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
           ok = false;
           break;
         }

@@ -10,8 +10,10 @@
 // the reads.
 //   warp 0     loads: its Q tile; its half of each 32 KB unit of K (128 keys by
 //              128 columns) and V (64 keys by 256 columns)
-//   warp 1     issues the MMAs: QK(j+1), PV(j)
-//   warps 2-5  softmax and output, a query row per thread
+//   warps 1, 2 issue the MMAs, one Q K^T, the other P V (a thread's issue takes
+//              about as long as the tensor pipe's work: one warp for both left
+//              the pipe idle)
+//   warps 3-6  softmax and output, a query row per thread
 // A unit's slot is refilled when both CTAs' MMAs have read it (their commits
 // arrive in both CTAs).
 #include "internal.h"
@@ -26,7 +28,7 @@ namespace {
 using namespace packed;
 
 constexpr int D = 256;
-constexpr int kThreads = 192;
+constexpr int kThreads = 224;
 constexpr int kUnits = 5;
 constexpr int kUnit = 32768;
 constexpr int kQBytes = kBM * D * 2;
@@ -43,11 +45,16 @@ struct Bars {
   uint64_t q_full, q_empty;
   uint64_t u_full[kUnits], u_empty[kUnits], v_land[kUnits];
   uint64_t s_full[2], p_full[2][2], pv_done[2];  // of each S; p_full of each half of its P
-  uint64_t o_full, o_free, drain;
+  uint64_t o_full, o_free, drain[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
+
+// Units leave in the order K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
+// two each: the first of K_j and of V_j.
+__device__ __forceinline__ int k_unit(int j) { return j == 0 ? 0 : 4 * j - 2; }
+__device__ __forceinline__ int v_unit(int j, int n) { return j == n - 1 ? 4 * n - 2 : 4 * j + 4; }
 
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     packed_tc_d256_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -78,7 +85,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     }
     ptx::mbar_init(&bar.o_full, 1);
     ptx::mbar_init(&bar.o_free, 128);
-    ptx::mbar_init(&bar.drain, 1);
+    for (int s = 0; s < 2; ++s) ptx::mbar_init(&bar.drain[s], 1);
     bar.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -166,79 +173,93 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     if (lane == 0 && *abort && nq) ptx::mbar_wait_bounded(&bar.q_full, (nq - 1) & 1, kWaitPolls >> 6);
     __syncwarp();
   } else if (warp == 1) {
-    // ---------------- MMAs ----------------
+    // ---------------- Q K^T ----------------
     if (lane == 0) {
-      const uint64_t qdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
-      const uint64_t kdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
-      const uint64_t vdesc0 = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 64 * 128, 1024);
-      int u = 0, nq = 0, cq = 0, cp = 0;  // units, items, QK and PV products issued
+      const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
+      const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
+      int base = 0, nq = 0, c = 0;  // first unit of the item, items, products so far
       bool ok = true, issued = false;
-      // the two units of a K or V tile, in load order
-      auto qk = [&](bool active, bool first) -> bool {
-        for (int part = 0; part < 2; ++part, ++u) {
-          const int s = u % kUnits;
-          if (!spin_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
-          ptx::tc_fence_after();
-          if (active) {
-            if (first && part == 0) {
-              if (!wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim)) return false;
-              ptx::tc_fence_after();
-            }
-            const uint64_t kd = kdesc0 + ((s * kUnit) >> 4);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const uint64_t qd = qdesc0 + (((2 * part + (k >> 2)) * (kBM * 128) + (k & 3) * 32) >> 4);
-              ptx::umma_bf16(tbase + (cq & 1) * kBN, qd, kd + (((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4), kIdescQK,
-                             part > 0 || k > 0);
-            }
-          }
-          ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
-        }
-        if (active) {
-          ptx::umma_commit(&bar.s_full[cq & 1]);
-          ++cq;
-        }
-        return true;
-      };
-      auto pv = [&](bool active, bool first) -> bool {
-        for (int part = 0; part < 2; ++part, ++u) {
-          const int s = u % kUnits;
-          if (!spin_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim)) return false;
-          if (active) {
-            if (part == 0 && first && nq > 1 && !wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim)) return false;
-            if (!spin_or_abort(&bar.p_full[cp & 1][part], (cp >> 1) & 1, abort, lim)) return false;
-            ptx::tc_fence_after();
-            const uint64_t vd = vdesc0 + ((s * kUnit) >> 4);
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-              ptx::umma_bf16_ts(tbase + kOCol, tbase + (cp & 1) * kBN + (part * 4 + k) * 8, vd + ((k * 2048) >> 4),
-                                kIdescPV, !first || part > 0 || k > 0);
-          }
-          ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
-        }
-        if (active) {
-          ptx::umma_commit(&bar.pv_done[cp & 1]);
-          ++cp;
-        }
-        return true;
-      };
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at(p, wi);
         const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
         issued = true;
         nq += lo < hi;
-        auto act = [&](int kt) { return kt >= lo && kt < hi; };
-        ok = qk(act(w.k_lo), w.k_lo == lo);
         for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
-          if (kt + 1 < w.k_hi && !(ok = qk(act(kt + 1), kt + 1 == lo))) break;
-          if (kt + 1 == hi - 1 || (kt == w.k_lo && kt == hi - 1)) ptx::umma_commit(&bar.q_empty);
-          if (!(ok = pv(act(kt), kt == lo))) break;
+          const int u = base + k_unit(kt - w.k_lo);
+          const bool active = kt >= lo && kt < hi;
+          if (active) {
+            if (kt == lo && !(ok = wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim))) break;
+            // the P that lay in this S has been read
+            if (c > 1 && !(ok = wait_or_abort(&bar.pv_done[c & 1], ((c >> 1) - 1) & 1, abort, lim))) break;
+          }
+          for (int part = 0; part < 2; ++part) {
+            const int s = (u + part) % kUnits;
+            if (!(ok = wait_or_abort(&bar.u_full[s], ((u + part) / kUnits) & 1, abort, lim))) break;
+            ptx::tc_fence_after();
+            if (active) {
+              const uint64_t kd = kdesc + ((s * kUnit) >> 4);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint64_t qd = qdesc + (((2 * part + (k >> 2)) * (kBM * 128) + (k & 3) * 32) >> 4);
+                ptx::umma_bf16(tbase + (c & 1) * kBN, qd, kd + (((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4), kIdescQK,
+                               part > 0 || k > 0);
+              }
+              if (part == 1) ptx::umma_commit(&bar.s_full[c & 1]);
+            }
+            ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
+          }
+          if (!ok) break;
+          c += active;
+          if (kt == hi - 1) ptx::umma_commit(&bar.q_empty);
+        }
+        base += 4 * (w.k_hi - w.k_lo);
+      }
+      // every MMA issued has completed before tensor memory is released
+      if (issued) {
+        ptx::umma_commit(&bar.drain[0]);
+        if (!ptx::mbar_wait_bounded(&bar.drain[0], 0, kWaitPolls)) *abort = 1;
+      }
+    }
+    __syncwarp();
+  } else if (warp == 2) {
+    // ---------------- P V ----------------
+    if (lane == 0) {
+      const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 64 * 128, 1024);
+      int base = 0, nq = 0, c = 0;
+      bool ok = true, issued = false;
+      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+        const Work w = work_at(p, wi);
+        const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0], n = w.k_hi - w.k_lo;
+        issued = true;
+        nq += lo < hi;
+        for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
+          const int u = base + v_unit(kt - w.k_lo, n);
+          const bool active = kt >= lo && kt < hi, first = kt == lo;
+          if (active && first && nq > 1 && !(ok = wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim))) break;
+          for (int part = 0; part < 2; ++part) {
+            const int s = (u + part) % kUnits;
+            if (!(ok = wait_or_abort(&bar.u_full[s], ((u + part) / kUnits) & 1, abort, lim))) break;
+            if (active) {
+              if (!(ok = wait_or_abort(&bar.p_full[c & 1][part], (c >> 1) & 1, abort, lim))) break;
+              ptx::tc_fence_after();
+              const uint64_t vd = vdesc + ((s * kUnit) >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                ptx::umma_bf16_ts(tbase + kOCol, tbase + (c & 1) * kBN + (part * 4 + k) * 8, vd + ((k * 2048) >> 4),
+                                  kIdescPV, !first || part > 0 || k > 0);
+              if (part == 1) ptx::umma_commit(&bar.pv_done[c & 1]);
+            }
+            ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
+          }
+          if (!ok) break;
+          c += active;
           if (kt == hi - 1) ptx::umma_commit(&bar.o_full);
         }
+        base += 4 * n;
       }
       if (issued) {
-        ptx::umma_commit(&bar.drain);
-        if (!ptx::mbar_wait_bounded(&bar.drain, 0, kWaitPolls)) *abort = 1;
+        ptx::umma_commit(&bar.drain[1]);
+        if (!ptx::mbar_wait_bounded(&bar.drain[1], 0, kWaitPolls)) *abort = 1;
       }
     }
     __syncwarp();
@@ -259,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (!valid) ra = rb = 0;
       float m = -INFINITY, l = 0.f;
       for (int kt = lo; kt < hi; ++kt, ++n) {
-        if (!(ok = __all_sync(0xffffffffu, spin_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
         ptx::tc_fence_after();
         ok = softmax_tile<D>(ts + (n & 1) * kBN, to, ra, rb, kt * kBN, p.c, m, l, [&] {
           const bool done =
