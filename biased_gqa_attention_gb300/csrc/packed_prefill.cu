@@ -122,14 +122,6 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
     const int h0 = static_cast<int>(w - at * p.heads) * p.pk, hk = h0 / p.g;
     const int2 keys = item_keys(p, item.len, item.tok0);
     st.clear();
-    for (int i = lane; i < kRows * D; i += 32) {
-      const int r = i / D, d = i - r * D, row = warp * kRows + r;
-      const int tok = item.tok0 + row / p.pk;
-      qs[i] = tok < item.len ? Elem<T>::load(static_cast<const T*>(p.q) + (item.row0 + tok) * p.q_stride +
-                                                 static_cast<int64_t>(h0 + row % p.pk) * D,
-                                             d) * p.c
-                             : 0.f;
-    }
     auto load = [&](int t, int s) {
       const int k0 = keys.x + t * KT;
       const uint32_t kd = ptx::smem_u32(ring + s * stage), vd = kd + KT * stride * sizeof(T);
@@ -147,6 +139,12 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
     const int nt = (keys.y - keys.x + KT - 1) / KT;
     load(0, 0);
     cp_async_commit();
+    simt_stage_q<T, DPL>(qs, D, p.c, [&](int r) -> const T* {
+      const int row = warp * kRows + r, tok = item.tok0 + row / p.pk;
+      return tok < item.len ? static_cast<const T*>(p.q) + (item.row0 + tok) * p.q_stride +
+                                  static_cast<int64_t>(h0 + row % p.pk) * D
+                            : nullptr;
+    });
     for (int t = 0; t < nt; ++t) {
       if (t + 1 < nt) load(t + 1, (t + 1) & 1);
       cp_async_commit();
@@ -165,9 +163,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
         any |= lo[r] < hi[r];
       }
       const T* kt = ring + (t & 1) * stage;
-      if (any) simt_tile<T, DPL, KT>(st, kt, kt + KT * stride, stride, qs, ps, D, lo, hi, kRows);
+      if (any) simt_tile<T, DPL, KT>(st, kt, kt + KT * stride, stride, qs, ps, D, lo, hi);
       __syncthreads();
     }
+    st.reduce();
 #pragma unroll
     for (int r = 0; r < kRows; ++r) {
       const int row = warp * kRows + r, tok = item.tok0 + row / p.pk;

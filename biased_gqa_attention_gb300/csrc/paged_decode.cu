@@ -872,11 +872,8 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
       open = true;
       t_first = cur.t;
       st.clear();
-      for (int i = lane; i < kRows * D; i += 32) {
-        const int r = i / D, d = i - r * D;
-        const T* q = static_cast<const T*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + gr * kRows + r) * D;
-        qs[i] = r < heads ? Elem<T>::load(q, d) * p.c : 0.f;
-      }
+      const T* q = static_cast<const T*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + gr * kRows) * D;
+      simt_stage_q<T, DPL>(qs, D, p.c, [&](int r) { return r < heads ? q + static_cast<int64_t>(r) * D : nullptr; });
     }
     __syncwarp();  // tile it - 1 has been read by every lane
     if (issued < n) issue();
@@ -899,13 +896,14 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
         lo[r] = a;
         hi[r] = b;
       }
-      simt_tile<T, DPL, KT>(st, kt, kt + KT * stride, stride, qs, ps, D, lo, hi, heads);
+      simt_tile<T, DPL, KT>(st, kt, kt + KT * stride, stride, qs, ps, D, lo, hi);
       left = b >= 32 ? 0u : left & (~0u << b);
     }
 
     const bool unit_end = cur.t == cur.tiles - 1;
     if (unit_end || it == n - 1) {
       const bool whole = unit_end && t_first == 0;
+      st.reduce();
       T* y = static_cast<T*>(p.y) + (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRows) * D;
       const int64_t at = (static_cast<int64_t>(slice) * 2 + slot) * kRows;
 #pragma unroll
@@ -966,6 +964,22 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
   // partial i of the unit, in rows of the workspace
   auto at = [&](int i) { return (static_cast<int64_t>(s0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.rows + r; };
 
+  // four columns of the first partials this thread adds up: on their way while
+  // the weights are computed
+  const int cols = D / 4, subs = kMergeThreads / cols;  // D <= 512: two at least
+  const int sub = tid / cols, c = tid - sub * cols;
+  const float4* part = reinterpret_cast<const float4*>(p.part) + c;
+  constexpr int kAhead = 8;
+  float4 v[kAhead];
+  auto fetch = [&](int i0) {
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * subs;
+      v[u] = sub < subs && i < n ? __ldcg(part + at(i) * cols) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+  };
+  fetch(sub);
+
   float M = -INFINITY;
   for (int i = tid; i < n; i += kMergeThreads) {
     const float m = __ldcg(&p.ml[at(i)].x);
@@ -993,29 +1007,20 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
 #pragma unroll
   for (int i = 0; i < kMergeThreads / 32; ++i) L += red[1][i];
 
-  const int cols = D / 4, subs = kMergeThreads / cols;  // D <= 512: two at least
-  const int sub = tid / cols, c = tid - sub * cols;
   float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (sub < subs) {
-    auto add = [&](int i, const float4& v) {
-      const float w = w_s[i];
-      a.x = fmaf(w, v.x, a.x);
-      a.y = fmaf(w, v.y, a.y);
-      a.z = fmaf(w, v.z, a.z);
-      a.w = fmaf(w, v.w, a.w);
-    };
-    const float4* part = reinterpret_cast<const float4*>(p.part) + c;
-    int i = sub;
-    for (; i + 7 * subs < n; i += 8 * subs) {
-      float4 v[8];
+  for (int i0 = sub; i0 < n; i0 += kAhead * subs) {
+    if (i0 != sub) fetch(i0);
 #pragma unroll
-      for (int u = 0; u < 8; ++u) v[u] = __ldcg(part + at(i + u * subs) * cols);
-#pragma unroll
-      for (int u = 0; u < 8; ++u) add(i + u * subs, v[u]);
+    for (int u = 0; u < kAhead; ++u) {
+      const int i = i0 + u * subs;
+      const float w = i < n ? w_s[i] : 0.f;
+      a.x = fmaf(w, v[u].x, a.x);
+      a.y = fmaf(w, v[u].y, a.y);
+      a.z = fmaf(w, v[u].z, a.z);
+      a.w = fmaf(w, v[u].w, a.w);
     }
-    for (; i < n; i += subs) add(i, __ldcg(part + at(i) * cols));
-    acc_s[tid] = a;
   }
+  if (sub < subs) acc_s[tid] = a;
   __syncthreads();
   if (sub == 0) {
     for (int u = 1; u < subs; ++u) {
