@@ -175,6 +175,48 @@ __device__ __forceinline__ Cursor<KT> cursor_at(const PagedParams& p, const int6
   return c;
 }
 
+// The same for at most 32 sequences, a lane each: every warp scans them for
+// itself, without meeting the block and without loading a length twice.
+template <int KT>
+struct LaneScan {
+  LiveKeys keys;
+  int64_t end;  // tiles (per unit) up to and with this lane's sequence
+  __device__ __forceinline__ explicit LaneScan(const PagedParams& p) {
+    const int lane = threadIdx.x & 31;
+    const int64_t np = lane < p.B ? p.nonpad[lane] : 0;
+    const bool bad = np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size;
+    const int n = bad ? 0 : static_cast<int>(np);
+    keys = {p.window > 0 && n > p.window ? n - p.window : 0, n};
+    const int64_t mine = tiles_of<KT>(keys);
+    end = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, end, o);
+      if (lane >= o) end += x;
+    }
+    if (p.B <= 32 && blockIdx.x == 0 && threadIdx.x < 32) {
+      if (lane < p.B) p.base[lane] = end - mine;
+      if (lane == 31) p.base[p.B] = end;
+      if (bad) report(p.status, EXTKV_DEV_BAD_NONPAD);
+    }
+  }
+  __device__ __forceinline__ int64_t total(const PagedParams& p) const {
+    return __shfl_sync(0xffffffffu, end, 31) * p.units;
+  }
+  // f is the warp's
+  __device__ __forceinline__ Cursor<KT> cursor_at(const PagedParams& p, int64_t f) const {
+    Cursor<KT> c;
+    c.b = __popc(__ballot_sync(0xffffffffu, end * p.units <= f));
+    c.keys.lo = __shfl_sync(0xffffffffu, keys.lo, c.b);
+    c.keys.hi = __shfl_sync(0xffffffffu, keys.hi, c.b);
+    c.tiles = tiles_of<KT>(c.keys);
+    const int64_t rest = f - (__shfl_sync(0xffffffffu, end, c.b) - c.tiles) * p.units;
+    c.u = static_cast<int>(Axis::div(rest, c.tiles));
+    c.t = static_cast<int>(rest - static_cast<int64_t>(c.u) * c.tiles);
+    return c;
+  }
+};
+
 // Pool rows of a tile, one per lane: the page id is loaded a tile ahead.
 template <int KT>
 struct TileRows {
@@ -294,7 +336,6 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   __shared__ int64_t pre[C::kThreads + 1], warp_sum[C::kThreads / 32];
   __shared__ uint32_t live_mask[W][NS];  // keys of the slot's K tile that were loaded
   __shared__ Rec rec[W];
-  __shared__ Cursor<KT> start_at[W];
   __shared__ Chain chains[W + 1];
   __shared__ int n_chains;
   __shared__ uint64_t full[W][NS], empty[W][NS];
@@ -316,22 +357,32 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
-  const int per = scan_tiles<KT>(p, pre, warp_sum);  // meets the whole block
-  const Axis axis(p, pre[blockDim.x] * p.units);
+  const bool few = p.B <= 32;
+  const LaneScan<KT> scan(p);  // (of the first 32 sequences where there are more: not used)
+  int per = 0;
+  if (few) __syncthreads();  // the barriers
+  else per = scan_tiles<KT>(p, pre, warp_sum);
+  const Axis axis(p, few ? scan.total(p) : pre[blockDim.x] * p.units);
   const int cta = blockIdx.x;
   if (cta >= axis.n) return;
   const int64_t c0 = axis.start(cta);
   const int tiles_here = static_cast<int>(axis.start(cta + 1) - c0);  // at least one
-  const int mine = C::TMA && warp == W ? min(lane, W - 1) : warp;     // the producer's lanes serve a warp each
-  const int i0 = static_cast<int>(static_cast<int64_t>(tiles_here) * mine / W);
-  const int n = static_cast<int>(static_cast<int64_t>(tiles_here) * (mine + 1) / W) - i0;
+  auto first_of = [&](int w) { return static_cast<int>(static_cast<int64_t>(tiles_here) * w / W); };
+  auto at_tile = [&](int64_t f) { return few ? scan.cursor_at(p, f) : cursor_at<KT>(p, pre, per, f); };
+  // a consumer's part; the producer's lanes serve a consumer each
   Cursor<KT> cur{};
-  if (warp < W && n > 0) cur = cursor_at<KT>(p, pre, per, c0 + i0);
-  if constexpr (C::TMA) {
-    if (warp < W && lane == 0) start_at[warp] = cur;
-    __syncthreads();
-    if (warp == W) cur = start_at[mine];
+  int mine = warp;
+  if (!C::TMA || warp < W) {
+    if (first_of(mine) < first_of(mine + 1)) cur = at_tile(c0 + first_of(mine));
+  } else {
+    mine = min(lane, W - 1);
+    for (int w = 0; w < W; ++w)
+      if (first_of(w) < first_of(w + 1)) {
+        const Cursor<KT> c = at_tile(c0 + first_of(w));
+        if (w == mine) cur = c;
+      }
   }
+  const int n = first_of(mine + 1) - first_of(mine);
 
   if (C::TMA && warp == W) {
     // ---------------- producer ----------------
@@ -813,8 +864,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, D = p.D;
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
-  const int per = scan_tiles<KT>(p, pre, warp_sum);
-  const Axis axis(p, pre[blockDim.x] * p.units);
+  const bool few = p.B <= 32;
+  const LaneScan<KT> scan(p);
+  int per = 0;
+  if (!few) per = scan_tiles<KT>(p, pre, warp_sum);
+  const Axis axis(p, few ? scan.total(p) : pre[blockDim.x] * p.units);
   const int slice = warp * gridDim.x + blockIdx.x;  // few tiles: one warp per SM first
   if (slice >= axis.n) return;
   const int64_t f0 = axis.start(slice), f1 = axis.start(slice + 1);
@@ -830,7 +884,7 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
   const int chunks = D * static_cast<int>(sizeof(T)) / 16;
   const int row_bytes = D * static_cast<int>(sizeof(T));
 
-  Cursor<KT> ld = cursor_at<KT>(p, pre, per, f0);
+  Cursor<KT> ld = few ? scan.cursor_at(p, f0) : cursor_at<KT>(p, pre, per, f0);
   Cursor<KT> cur = ld;
   TileRows<KT> rows;
   rows.look_up(p, ld);
@@ -1085,7 +1139,7 @@ cudaError_t launch_mma_cfg(PagedParams p, cudaStream_t s) {
     p.box = p.page_size % C::KT == 0 ? C::KT : 16;
     const uint64_t dims[4] = {64, static_cast<uint64_t>(p.page_size), static_cast<uint64_t>(p.num_pages) * p.Hkv, C::D / 64};
     const uint64_t str[3] = {C::D * 2, static_cast<uint64_t>(p.page_size) * C::D * 2, 128};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(p.box), 1, p.box == C::KT ? C::D / 64 : 1};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(p.box), 1, p.box == C::KT ? C::D / 64u : 1u};
     if (!make_tensor_map_bf16(&kmap, p.k, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map_bf16(&vmap, p.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;

@@ -439,6 +439,11 @@ def _need_rows(t, name, shape, dtype) -> int:
     return t.stride(0) if rows > 1 else H * D
 
 
+def _window(window) -> int:
+    """A window of 2^31 keys or more masks nothing that one of 2^31 - 1 does not."""
+    return max(0, min(int(window), 2 ** 31 - 1))
+
+
 def _need_status(status):
     _need(status, "status", dtype=torch.int32)
     if status is not None and status.numel() < 4:
@@ -597,7 +602,7 @@ def _marshal_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, win
     workspace = _need_workspace(workspace, attention_paged_decode_workspace_size(B, Hq, Hkv, D, q.dtype), q.device,
                                 stream)
     return load().attention_paged_decode, (_p(y), _p(q), _p(k_pages), _p(v_pages), _p(page_table), _p(nonpad),
-                                           float(scale), int(window), B, Hq, Hkv, D, num_pages, page_size,
+                                           float(scale), _window(window), B, Hq, Hkv, D, num_pages, page_size,
                                            page_table.shape[1], qs, dt, _p(workspace), _ws_bytes(workspace),
                                            _p(status), _stream(stream)), \
         (workspace, y, q, k_pages, v_pages, page_table, nonpad, status)
@@ -650,7 +655,7 @@ def _marshal_packed_prefill(y, q, k, v, cu_seqlens, scale, causal, window, works
     workspace = _need_workspace(workspace, attention_packed_prefill_workspace_size(T, B, Hq, Hkv, D, q.dtype),
                                 q.device, stream)
     return load().attention_packed_prefill, (_p(y), _p(q), _p(k), _p(v), _p(cu_seqlens), float(scale),
-                                             int(bool(causal)), int(window), T, B, Hq, Hkv, D, qs, ks, vs, dt,
+                                             int(bool(causal)), _window(window), T, B, Hq, Hkv, D, qs, ks, vs, dt,
                                              _p(workspace), _ws_bytes(workspace), _p(status), _stream(stream)), \
         (workspace, y, q, k, v, cu_seqlens, status)
 

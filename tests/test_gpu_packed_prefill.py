@@ -94,6 +94,11 @@ CASES = [
     (EDGES, 4, 2, 64, torch.float32, True, 0, False, 0, 0),
     (EDGES, 6, 2, 128, torch.float32, False, 0, True, 3, 3),
     (EDGES, 4, 1, 264, torch.float32, True, 40, False, 0, 0),
+    ((5, 0, 33, 2), 128, 1, 64, torch.bfloat16, True, 0, True, 0, 3),     # a token a query tile
+    ((5, 0, 33, 2), 64, 2, 256, torch.bfloat16, True, 7, False, 0, 0),
+    ((5, 0, 33, 2), 96, 1, 128, torch.bfloat16, False, 0, False, 1, 0),
+    ((40, 3), 64, 1, 64, torch.float32, True, 0, False, 0, 0),
+    (EDGES, 4, 2, 128, torch.bfloat16, True, 2 ** 32 + 5, False, 0, 0),  # a window past every length
     ((1,), 1, 1, 64, torch.bfloat16, True, 0, False, 0, 0),
     ((1,), 1, 1, 8, torch.float32, True, 0, False, 0, 0),
     ((2500,), 4, 2, 128, torch.bfloat16, True, 0, False, 0, 0),

@@ -91,6 +91,9 @@ CASES = [
     (MIX, 22, 2, 128, 24, 0, torch.float32),
     (MIX, 4, 2, 200, 16, 100, torch.float32),
     (MIX, 9, 1, 512, 5, 0, torch.float32),
+    (MIX, 128, 1, 64, 16, 2 ** 32 + 5, torch.bfloat16),   # a window past every length; eight row groups
+    (MIX, 64, 1, 256, 48, 0, torch.bfloat16),     # a page of one and a half tiles of 32, three of 16
+    (MIX, 2, 1, 64, 48, 50, torch.bfloat16),
     ((1,), 1, 1, 64, 16, 0, torch.bfloat16),
     ((1,), 1, 1, 8, 16, 0, torch.float32),
     ((20011,), 16, 8, 256, 16, 0, torch.bfloat16),          # one sequence over every slice
@@ -182,6 +185,17 @@ def test_bad_lengths_and_pages_are_flagged_and_skipped(dtype, D):
     y = torch.full_like(good, 7.0)
     ek.attention_paged_decode(y, q, k, v, t2, nonpad, scale)
     assert torch.count_nonzero(y[2]) == 0 and torch.isfinite(y.float()).all()
+
+
+def test_the_length_limits():
+    """Full tables: every slot of every page live, lengths at the capacity."""
+    for D, page, dtype in ((128, 16, torch.bfloat16), (256, 5, torch.bfloat16), (64, 16, torch.float32)):
+        lens = (page * 9, page * 9)
+        q, k, v, table, nonpad = make(lens, 4, 2, D, page, dtype)
+        table = table[:, :9].contiguous()
+        y = run(q, k, v, table, nonpad, 0.1, 0)
+        ref, tol = reference(q, k, v, table, lens, 0, 0.1)
+        check(y, ref, tol, "full")
 
 
 def test_an_empty_table_and_an_empty_batch():

@@ -215,3 +215,36 @@ def test_rows_outside_every_sequence_are_left():
     assert ek.extkv_read_status(st) == ek.EXTKV_OK
     assert (qo[10:] == 7.0).all() and not (qo[:10] == 7.0).all()
     assert torch.equal(v2, scatter_plain(vp, v[:10], table, starts, lens, page))
+
+
+def test_append_captured_and_on_another_stream():
+    lens, starts, page, D = (1, 1, 1), (4, 100, 0), 16, 128
+    gen = torch.Generator().manual_seed(6)
+    q, k, v, kp, vp, table, widx, cu = append_inputs(lens, starts, 8, 2, D, page, torch.bfloat16, gen)
+    pos = widx[None].repeat(3, 1).contiguous()
+    spec = ek.RotarySpec(pos, inv_freq(64).cuda(), (16, 24, 24))
+    want_k, want_v, want_q = kp.clone(), vp.clone(), torch.empty((3, 8, D), dtype=torch.bfloat16, device="cuda")
+    ek.paged_kv_append(want_k, want_v, k, v, table, widx, rotary=spec, q_out=want_q, q=q)
+    got_k, got_v, got_q = kp.clone(), vp.clone(), torch.zeros_like(want_q)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    ek.paged_kv_append(got_k, got_v, k, v, table, widx, rotary=spec, q_out=got_q, q=q, stream=s)
+    s.synchronize()
+    assert torch.equal(got_k, want_k) and torch.equal(got_v, want_v) and torch.equal(got_q, want_q)
+    got_k.copy_(kp)
+    got_v.copy_(vp)
+    got_q.zero_()
+    call = ek.prepare_paged_kv_append(got_k, got_v, k, v, table, widx, rotary=spec, q_out=got_q, q=q, stream=s)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=s):
+        call()
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got_k, want_k) and torch.equal(got_v, want_v) and torch.equal(got_q, want_q)
+    # the slots may move between replays
+    widx += 1
+    pos += 1
+    g.replay()
+    ek.paged_kv_append(want_k, want_v, k, v, table, widx, rotary=spec, q_out=want_q, q=q)
+    torch.cuda.synchronize()
+    assert torch.equal(got_k, want_k) and torch.equal(got_v, want_v) and torch.equal(got_q, want_q)
