@@ -6,24 +6,25 @@
 //
 // A persistent CTA per SM takes query tiles from the plan's list (dearest
 // first, rounds taken in alternating order).  An item is 256 query rows, two
-// M = 128 tiles A and B of one KV head's (token, head) rows: while one tile's
-// scores go through the softmax, the tensor cores work for the other.
-//   warp 0       loads: Q tiles, then K and V tiles of 128 keys through a ring
-//                of shared-memory units (TMA, 128-byte swizzle)
-//   warps 1, 2   issue the MMAs of tile A and of tile B: PV(j-1), QK(j) for each
-//                key tile; S and O live in tensor memory, P (bf16) over the
-//                first half of its S.  Issuing a 128 x 128 x 16 MMA costs its
-//                thread longer than the tensor pipe takes for it (64 cycles),
-//                so one thread for both tiles left the pipe idle half the time
-//   warps 4-7    softmax and output of tile A, a query row per thread
-//   warps 8-11   the same for tile B
-// (warp 3 only fills the first warpgroup, which gives its registers to the other
-// two: 72 against 216 of the 168 a thread the block starts with.)
-// The tensor pipe runs a thread's MMAs in order, so S_t(j) being complete
-// implies that PV_t(j-1) is: a softmax warp may rescale O_t before it releases
-// P_t(j) without another barrier.  O is rescaled only when a row's maximum has
-// grown by more than 8 in the exponent (P then stays below 2^8, exact enough in
-// bf16 and fp32 alike).
+// M = 128 tiles A and B of one KV head's (token, head) rows.
+//   warp 0       loads: Q tiles, then K and V tiles of KN keys through a ring of
+//                shared-memory units (TMA, 128-byte swizzle)
+//   warps 1, 2   issue Q K^T of tile A and of tile B
+//   warps 4, 5   issue P V of tile A and of tile B
+//   warps 8-11   softmax and output of tile A, a query row per thread
+//   warps 12-15  the same for tile B
+// (warps 3, 6 and 7 only fill warpgroups: the first two give registers to the
+// softmax's.)
+// Tensor memory holds S, P (bf16) and O of each tile apart from each other, so
+// the two products of a tile depend on each other only through the softmax:
+// QK(j + 1) is issued as soon as the softmax has S(j) in registers and runs
+// beside it.  That is what fixes KN at head size 128: 80 + 40 + 128 columns, of
+// 256 a tile.  Four issuers, because a thread's barrier tests (some hundred
+// cycles each) stand between its products, and the pipe empties meanwhile:
+// measured alone it takes one 128 x 128 x 16 MMA every 64 cycles from one thread.
+// A 16001-token prompt of 8 heads of 128: 515 us with one issuer and P over an S
+// of 128 keys, 462 us with one per tile, 486 us with S and P apart, 391 us so
+// (1340 TFLOP/s, 0.70 of the measured cuBLAS rate).
 #include "internal.h"
 #include "packed_tc.cuh"
 #include "packed_tc.h"
@@ -39,15 +40,20 @@ constexpr int kMaxUnits = 8;
 
 template <int D>
 struct Cfg {
-  static constexpr int kThreads = 384;
-  static constexpr int kTile = kBM * D * 2;  // bytes of a Q, K or V tile
-  static constexpr int kUnits = (232448 - 2048 - 2 * kTile) / kTile < kMaxUnits ? (232448 - 2048 - 2 * kTile) / kTile : kMaxUnits;
-  static constexpr int kOffKV = 2 * kTile;
+  static constexpr int kThreads = 512;
+  static constexpr int KN = D == 64 ? 128 : 80;  // keys of a tile
+  static constexpr int kPart = D == 64 ? 64 : 48;  // keys of P released first
+  static constexpr int kQTile = kBM * D * 2, kTile = KN * D * 2;  // bytes of a Q and of a K or V tile
+  static constexpr int kFit = (232448 - 2048 - 2 * kQTile) / kTile;
+  static constexpr int kUnits = kFit < kMaxUnits ? kFit : kMaxUnits;
+  static constexpr int kOffKV = 2 * kQTile;
   static constexpr int kOffBar = kOffKV + kUnits * kTile;
   static constexpr int kSmem = kOffBar + 512 + 1024;
-  static constexpr uint32_t kOCol = 256;  // S_A, S_B at 0 and 128; O_A, O_B from here
+  // tensor memory of a tile: S, P, O
+  static constexpr uint32_t kStride = 256, kPCol = KN, kOCol = kStride - D;
   static constexpr uint32_t kTmemCols = 512;
-  static constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0, 0);
+  static constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, KN, 0, 0);
+  static_assert(kPCol + KN / 2 <= kOCol, "tensor memory columns");
   static constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, D, 0, 1);
   static_assert(kSmem <= 232448 && kUnits >= 4, "shared memory");
 };
@@ -55,14 +61,14 @@ struct Cfg {
 struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t u_full[kMaxUnits], u_empty[kMaxUnits];
-  uint64_t s_full[2], p_full[2][2], o_full[2], o_free[2];  // p_full: of each half of P
-  uint64_t v_tail, drain[2];
+  uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_free[2];  // p_full: of each part of P
+  uint64_t v_tail, drain[4];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
-// Registers of the calling warpgroup; 128 * 72 + 256 * 216 = 384 * 168.
+// Registers of the calling warpgroup; 256 * 72 + 256 * 176 <= 512 * 128.
 template <int N>
 __device__ __forceinline__ void reg_dec() {
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
@@ -77,6 +83,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const PackedParams p) {
   using C = Cfg<D>;
+  constexpr int KN = C::KN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bar = *reinterpret_cast<Bars*>(sm + C::kOffBar);
@@ -90,6 +97,8 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_init(&bar.q_full[t], 1);
       ptx::mbar_init(&bar.q_empty[t], 1);
       ptx::mbar_init(&bar.s_full[t], 1);
+      ptx::mbar_init(&bar.s_free[t], 4);
+      ptx::mbar_init(&bar.pv_done[t], 1);
       ptx::mbar_init(&bar.p_full[t][0], 4);
       ptx::mbar_init(&bar.p_full[t][1], 4);
       ptx::mbar_init(&bar.o_full[t], 1);
@@ -100,7 +109,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_init(&bar.u_empty[u], 2);
     }
     ptx::mbar_init(&bar.v_tail, 1);
-    for (int t = 0; t < 2; ++t) ptx::mbar_init(&bar.drain[t], 1);
+    for (int t = 0; t < 4; ++t) ptx::mbar_init(&bar.drain[t], 1);
     bar.abort = 0;
     ptx::fence_mbar_init();
   }
@@ -121,7 +130,14 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
   const int tt = p.tile_tok / 2;
 
-  if (warp < 4) {
+  // every MMA an issuer issued has completed before tensor memory is released
+  auto drain = [&](bool issued, int who) {
+    if (!issued) return;
+    ptx::umma_commit(&bar.drain[who - 1]);
+    if (!ptx::mbar_wait_bounded(&bar.drain[who - 1], 0, kWaitPolls)) *abort = 1;
+  };
+
+  if (warp < 8) {
     reg_dec<72>();
     if (warp == 0) {
     // ---------------- loads ----------------
@@ -133,18 +149,18 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     auto load_q = [&](const Work& w, int t) -> bool {
       if (w.lo[t] >= w.hi[t]) return true;
       if (nq[t] && !wait_or_abort(&bar.q_empty[t], (nq[t] - 1) & 1, abort, lim)) return false;
-      ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kTile);
-      ptx::tma_load_4d(sm + t * C::kTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
+      ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kQTile);
+      ptx::tma_load_4d(sm + t * C::kQTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
       ++nq[t];
       return true;
     };
     Rounds rounds(n_work, blockIdx.x, gridDim.x);
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at(p, wi);
+      const Work w = work_at<KN>(p, wi);
       if (lane == 0) ok = load_q(w, 0);
       for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
-        const int key0 = w.row0 + kt * kBN;
-        const bool tail = (kt + 1) * kBN > w.len;  // keys of the next sequence behind the last one
+        const int key0 = w.row0 + kt * KN;
+        const bool tail = (kt + 1) * KN > w.len;  // keys of the next sequence behind the last one
         if (lane == 0) {
           ok = ok && acquire();
           if (ok) {
@@ -171,7 +187,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (tail) {
           if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_tail, tails & 1, abort, lim)))) break;
           ++tails;
-          zero_rows<D>(dst, w.len - kt * kBN, kBN, lane);
+          zero_rows<D>(dst, w.len - kt * KN, KN, lane);
           if (lane == 0) ptx::mbar_arrive(&bar.u_full[u % C::kUnits]);
         }
         ++u;
@@ -185,86 +201,98 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
     }
     __syncwarp();
-  } else if (warp < 3) {
-    // ---------------- MMAs of one query tile ----------------
-    if (lane == 0) {
-      const int t = warp - 1;
-      const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm + t * C::kTile), 16, 1024);
-      const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
-      const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kBN * 128, 1024);
-      const uint32_t ts = tbase + t * kBN, to = tbase + C::kOCol + t * D;
-      int u = 0, nq = 0, np = 0;
-      bool ok = true, issued = false;
-      auto landed = [&](int x) { return wait_or_abort(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, abort, lim); };
-      Rounds rounds(n_work, blockIdx.x, gridDim.x);
-      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at(p, wi);
-        const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
-        issued = true;
-        nq += lo < hi;
-        for (int kt = w.k_lo; kt <= w.k_hi; ++kt) {
-          // P(kt-1) V(kt-1), then Q K(kt)^T over the S that held P(kt-1); K and V
-          // are waited for first, they are mostly there
-          const bool pv = kt > lo && kt <= hi, qk = kt >= lo && kt < hi;
-          if (!(ok = kt == w.k_lo || landed(u - 1)) || !(ok = kt == w.k_hi || landed(u))) break;
-          if (pv) {
-            const bool first = kt - 1 == lo;
-            if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free[t], (nq - 2) & 1, abort, lim))) break;
-            const uint64_t vd = vdesc + ((((u - 1) % C::kUnits) * C::kTile) >> 4);
-            for (int h = 0; h < 2 && ok; ++h) {  // the first half of the keys while the second goes through the softmax
-              if (!(ok = wait_or_abort(&bar.p_full[t][h], np & 1, abort, lim))) break;
+    } else if (warp < 3) {
+      // ---------------- Q K^T of one query tile ----------------
+      if (lane == 0) {
+        const int t = warp - 1;
+        const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm + t * C::kQTile), 16, 1024);
+        const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
+        const uint32_t ts = tbase + t * C::kStride;
+        int u = 0, nq = 0, c = 0;  // unit of the next K tile, items, products so far
+        bool ok = true, issued = false;
+        Rounds rounds(n_work, blockIdx.x, gridDim.x);
+        for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+          const Work w = work_at<KN>(p, wi);
+          const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
+          issued = true;
+          nq += lo < hi;
+          for (int kt = w.k_lo; kt < w.k_hi; ++kt, u += 2) {
+            if (!(ok = wait_or_abort(&bar.u_full[u % C::kUnits], (u / C::kUnits) & 1, abort, lim))) break;
+            if (kt >= lo && kt < hi) {
+              if (kt == lo && !(ok = wait_or_abort(&bar.q_full[t], (nq - 1) & 1, abort, lim))) break;
+              // the scores before these are in the softmax's registers
+              if (c > 0 && !(ok = wait_or_abort(&bar.s_free[t], (c - 1) & 1, abort, lim))) break;
               ptx::tc_fence_after();
+              const uint64_t kd = kdesc + (((u % C::kUnits) * C::kTile) >> 4);
 #pragma unroll
-              for (int k = 0; k < kBN / 32; ++k) {
-                const int ks = h * (kBN / 32) + k;
-                ptx::umma_bf16_ts(to, ts + ks * 8, vd + ((ks * 2048) >> 4), C::kIdescPV, (!first || ks > 0) ? 1u : 0u);
-              }
+              for (int k = 0; k < D / 16; ++k)
+                ptx::umma_bf16(ts, qdesc + (((k >> 2) * (kBM * 128) + (k & 3) * 32) >> 4),
+                               kd + (((k >> 2) * (KN * 128) + (k & 3) * 32) >> 4), C::kIdescQK, k > 0);
+              ptx::umma_commit(&bar.s_full[t]);
+              ++c;
+              if (kt == hi - 1) ptx::umma_commit(&bar.q_empty[t]);
             }
-            if (!ok) break;
-            ++np;
-            if (kt == hi) ptx::umma_commit(&bar.o_full[t]);
-          }
-          if (qk) {
-            if (kt == lo && !(ok = wait_or_abort(&bar.q_full[t], (nq - 1) & 1, abort, lim))) break;
-            ptx::tc_fence_after();
-            const uint64_t kd = kdesc + (((u % C::kUnits) * C::kTile) >> 4);
-#pragma unroll
-            for (int k = 0; k < D / 16; ++k) {
-              const uint32_t off = ((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4;
-              ptx::umma_bf16(ts, qdesc + off, kd + off, C::kIdescQK, k > 0);
-            }
-            ptx::umma_commit(&bar.s_full[t]);
-            if (kt == hi - 1) ptx::umma_commit(&bar.q_empty[t]);
-          }
-          // the slots' commits behind the products: S is what the softmax waits for
-          if (kt > w.k_lo) ptx::umma_commit(&bar.u_empty[(u - 1) % C::kUnits]);
-          if (kt < w.k_hi) {
             ptx::umma_commit(&bar.u_empty[u % C::kUnits]);
-            u += 2;
           }
         }
+        drain(issued, warp);
       }
-      // every MMA issued has completed before tensor memory is released
-      if (issued) {
-        ptx::umma_commit(&bar.drain[t]);
-        if (!ptx::mbar_wait_bounded(&bar.drain[t], 0, kWaitPolls)) *abort = 1;
+      __syncwarp();
+    } else if (warp == 4 || warp == 5) {
+      // ---------------- P V of one query tile ----------------
+      if (lane == 0) {
+        const int t = warp - 4;
+        const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), KN * 128, 1024);
+        const uint32_t tp = tbase + t * C::kStride + C::kPCol, to = tbase + t * C::kStride + C::kOCol;
+        int u = 1, nq = 0, c = 0;  // unit of the next V tile, items, products so far
+        bool ok = true, issued = false;
+        Rounds rounds(n_work, blockIdx.x, gridDim.x);
+        for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+          const Work w = work_at<KN>(p, wi);
+          const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
+          issued = true;
+          nq += lo < hi;
+          for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt, u += 2) {
+            if (!(ok = wait_or_abort(&bar.u_full[u % C::kUnits], (u / C::kUnits) & 1, abort, lim))) break;
+            if (kt >= lo && kt < hi) {
+              const bool first = kt == lo;
+              if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free[t], (nq - 2) & 1, abort, lim))) break;
+              const uint64_t vd = vdesc + (((u % C::kUnits) * C::kTile) >> 4);
+#pragma unroll
+              for (int k = 0; k < KN / 16; ++k) {
+                // the first part of the keys while the others go through the softmax
+                if (k == 0 || k == C::kPart / 16) {
+                  if (!(ok = wait_or_abort(&bar.p_full[t][k > 0], c & 1, abort, lim))) break;
+                  ptx::tc_fence_after();
+                }
+                ptx::umma_bf16_ts(to, tp + k * 8, vd + ((k * 2048) >> 4), C::kIdescPV, (!first || k > 0) ? 1u : 0u);
+              }
+              if (!ok) break;
+              ptx::umma_commit(&bar.pv_done[t]);
+              ++c;
+              if (kt == hi - 1) ptx::umma_commit(&bar.o_full[t]);
+            }
+            ptx::umma_commit(&bar.u_empty[u % C::kUnits]);
+          }
+        }
+        drain(issued, warp - 1);
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
   } else {
     // ---------------- softmax and output ----------------
-    reg_inc<216>();
-    const int t = (warp - 4) >> 2;
+    reg_inc<176>();
+    const int t = (warp - 8) >> 2;
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tbase + lane_base + t * kBN, to = tbase + lane_base + C::kOCol + t * D;
+    const uint32_t ts = tbase + lane_base + t * C::kStride, tp = ts + C::kPCol, to = ts + C::kOCol;
     const float c = p.c;
-    int ns = 0, no = 0;
+    const uint64_t c2 = ptx::f2(c, c);
+    int n = 0, no = 0;  // score tiles and items so far
     bool ok = true;
     Rounds rounds(n_work, blockIdx.x, gridDim.x);
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at(p, wi);
+      const Work w = work_at<KN>(p, wi);
       const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
       if (lo >= hi) continue;
       const int tok = w.tok0 + t * tt + row / p.pk;
@@ -273,19 +301,47 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       const bool valid = tok < w.len;
       if (!valid) ra = rb = 0;
       float m = -INFINITY, l = 0.f;
-      for (int kt = lo; kt < hi; ++kt) {
-        const int k0 = kt * kBN;
-        if (!__all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], ns & 1, abort, lim))) {
-          ok = false;
-          break;
-        }
-        ++ns;
+      for (int kt = lo; kt < hi; ++kt, ++n) {
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], n & 1, abort, lim)))) break;
         ptx::tc_fence_after();
-        // PV_t(kt - 1) is complete: S_t(kt) was issued after it
-        softmax_tile<D>(ts, to, ra, rb, k0, c, m, l, [] { return true; },
-                        [&](int h) {
-                          if (lane == 0) ptx::mbar_arrive(&bar.p_full[t][h]);
-                        });
+        Scores<KN> s;
+        s.load(ts);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar.s_free[t]);
+        s.mask(ra, rb, kt * KN);
+        // PV(n - 1) is complete: P may be written, O rescaled
+        bool p_free = n == 0;
+        auto pv_complete = [&] {
+          if (!p_free) {
+            p_free = __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done[t], (n - 1) & 1, abort, lim));
+            ptx::tc_fence_after();
+          }
+          return p_free;
+        };
+        if (!(ok = take_max<D>(s.max(), to, c, m, l, pv_complete))) break;
+        const float nm = m == -INFINITY ? 0.f : -m * c;
+        const uint64_t nm2 = ptx::f2(nm, nm);
+        uint64_t ls[4] = {0, 0, 0, 0};
+        uint32_t pk[C::kPart / 2];
+        s.template weights<0, C::kPart>(c2, nm2, ls, pk);
+        if (!(ok = pv_complete())) break;
+        if constexpr (C::kPart == 64) {
+          ptx::tmem_st32(tp, pk);
+        } else {
+          ptx::tmem_st16(tp, *reinterpret_cast<uint32_t(*)[16]>(pk));
+          ptx::tmem_st8(tp + 16, *reinterpret_cast<uint32_t(*)[8]>(pk + 16));
+        }
+        p_written();
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[t][0]);
+        uint32_t pk1[(KN - C::kPart) / 2];
+        s.template weights<C::kPart, KN - C::kPart>(c2, nm2, ls, pk1);
+        if constexpr (KN - C::kPart == 64) ptx::tmem_st32(tp + C::kPart / 2, pk1);
+        else ptx::tmem_st16(tp + C::kPart / 2, pk1);
+        p_written();
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[t][1]);
+        const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+        l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
       }
       if (!ok) break;
       if (!__all_sync(0xffffffffu, wait_or_abort(&bar.o_full[t], no & 1, abort, lim))) {
@@ -324,7 +380,7 @@ cudaError_t launch(const PackedParams& p, cudaStream_t s) {
   const uint64_t k_dims[4] = {64, T, static_cast<uint64_t>(p.Hkv), chunks};
   const uint64_t k_str[3] = {static_cast<uint64_t>(p.k_stride) * 2, D * 2, 128};
   const uint64_t v_str[3] = {static_cast<uint64_t>(p.v_stride) * 2, D * 2, 128};
-  const uint32_t k_box[4] = {64, kBN, 1, static_cast<uint32_t>(chunks)};
+  const uint32_t k_box[4] = {64, C::KN, 1, static_cast<uint32_t>(chunks)};
   if (!make_tensor_map_bf16(&qmap, p.q, 4, q_dims, q_str, q_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&kmap, p.k, 4, k_dims, k_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&vmap, p.v, 4, k_dims, v_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B))

@@ -15,6 +15,7 @@ constexpr float kGrow = 8.f;  // log2 units
 
 // Bounded wait that also gives up once another role has aborted.
 __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
+  if (limit > 0 && ptx::mbar_test_wait(bar, parity)) return true;  // cheaper than a suspending wait when it is there
   for (uint32_t i = 0; i < limit; ++i) {
     if (ptx::mbar_try_wait(bar, parity)) return true;
     if ((i & 127u) == 127u && *abort) return false;
@@ -23,22 +24,15 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
   return false;
 }
 
-// The same, polling without suspending at first: a poll sees the phase some
-// hundred cycles earlier.
-__device__ __forceinline__ bool spin_or_abort(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t limit) {
-  for (uint32_t i = 0; i < limit && i < 4096; ++i)
-    if (ptx::mbar_test_wait(bar, parity)) return true;
-  return wait_or_abort(bar, parity, abort, limit);
-}
-
 // One entry of the work list for one head group: two query tiles of
 // tile_tok / 2 tokens each.
 struct Work {
   int row0, len, tok0, h0, hk;
-  int lo[2], hi[2];  // key tiles of query tiles A and B (empty: tile B has no tokens)
+  int lo[2], hi[2];  // key tiles (of KN keys) of query tiles A and B (empty: tile B has no tokens)
   int k_lo, k_hi;    // their union
 };
 
+template <int KN>
 __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
   Work r;
   const int64_t at = w / p.heads;
@@ -56,8 +50,8 @@ __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
     const int t0 = it.tok0 + t * tt, t1 = min(it.len, t0 + tt);
     r.lo[t] = r.hi[t] = 0;
     if (t0 < t1) {
-      r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / kBN;
-      r.hi[t] = ((p.causal ? t1 : it.len) + kBN - 1) / kBN;
+      r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / KN;
+      r.hi[t] = ((p.causal ? t1 : it.len) + KN - 1) / KN;
       r.k_lo = min(r.k_lo, r.lo[t]);
       r.k_hi = max(r.k_hi, r.hi[t]);
     }
@@ -80,42 +74,60 @@ struct Rounds {
   }
 };
 
-// The softmax of one query row over one key tile: reads its 128 scores (raw
-// q.k) from tensor memory at `ts`, writes P (bf16) over the first 64 columns,
-// keeps the row's maximum m (raw) and sum l, and rescales the row of O at `to`
-// (D columns) when the maximum has grown by more than kGrow, so that P stays
-// below 2^8.  [ra, rb): the row's keys; k0: the tile's first; c: scale * log2(e).
-// `o_ready` is asked before O is rescaled: the product that last wrote it must
-// be complete (false: that wait gave up, and so does this).  `release(h)` runs,
-// with the warp together, when half h of P (64 keys) can be read.
-template <int D, class F, class G>
-__device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, int ra, int rb, int k0, float c, float& m,
-                                             float& l, F o_ready, G release) {
-  uint32_t s[4][32];
+// One query row's scores over KN keys (raw q.k), in registers.
+template <int KN>
+struct Scores {
+  static_assert(KN == 80 || KN == 128, "whole tensor-memory loads");
+  static constexpr int Q = (KN + 31) / 32;
+  uint32_t s[Q][32];
+  __device__ __forceinline__ float at(int e) const { return __uint_as_float(s[e >> 5][e & 31]); }
+  // from tensor memory at `ts`; keys outside [ra, rb) masked (k0: the first key)
+  __device__ __forceinline__ void load(uint32_t ts) {
 #pragma unroll
-  for (int q = 0; q < 4; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
-  ptx::tmem_wait_ld();
-  if (!__all_sync(0xffffffffu, ra <= k0 && rb >= k0 + kBN)) {
+    for (int q = 0; q < KN / 32; ++q) ptx::tmem_ld32(ts + 32 * q, s[q]);
+    if constexpr (KN % 32) ptx::tmem_ld16(ts + KN / 32 * 32, *reinterpret_cast<uint32_t(*)[16]>(s[Q - 1]));
+    ptx::tmem_wait_ld();
+  }
+  __device__ __forceinline__ void mask(int ra, int rb, int k0) {
+    if (__all_sync(0xffffffffu, ra <= k0 && rb >= k0 + KN)) return;
     const int a = ra - k0;
     const unsigned n = rb > ra ? rb - ra : 0;
 #pragma unroll
-    for (int q = 0; q < 4; ++q)
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        if (static_cast<unsigned>(32 * q + e - a) >= n) s[q][e] = 0xff800000u;
+    for (int e = 0; e < KN; ++e)
+      if (static_cast<unsigned>(e - a) >= n) s[e >> 5][e & 31] = 0xff800000u;
   }
-  float mt[4];
+  __device__ __forceinline__ float max() const {
+    float x[4] = {at(0), at(1), at(2), at(3)};
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    float x0 = __uint_as_float(s[q][0]), x1 = __uint_as_float(s[q][1]);
+    for (int e = 4; e < KN; e += 8) {
 #pragma unroll
-    for (int e = 2; e < 32; e += 4) {
-      x0 = ptx::max3(x0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-      if (e + 3 < 32) x1 = ptx::max3(x1, __uint_as_float(s[q][e + 2]), __uint_as_float(s[q][e + 3]));
+      for (int i = 0; i < 4; ++i)
+        x[i] = e + 4 + i < KN ? ptx::max3(x[i], at(e + i), at(e + 4 + i)) : fmaxf(x[i], at(e + i));
     }
-    mt[q] = fmaxf(x0, x1);
+    return fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
   }
-  const float m_new = fmaxf(m, ptx::max3(mt[0], mt[1], fmaxf(mt[2], mt[3])));
+  // weights of keys E0 .. E0 + N - 1 against the maximum in nm = -m * c, as packed
+  // bf16 (2^-8 of each weight off at most); ls sums them unrounded
+  template <int E0, int N>
+  __device__ __forceinline__ void weights(uint64_t c2, uint64_t nm2, uint64_t (&ls)[4], uint32_t (&pk)[N / 2]) const {
+#pragma unroll
+    for (int x = 0; x < N / 2; ++x) {
+      const uint64_t d = ptx::fma2(ptx::f2(at(E0 + 2 * x), at(E0 + 2 * x + 1)), c2, nm2);
+      const float e0 = ptx::ex2(ptx::f2_lo(d)), e1 = ptx::ex2(ptx::f2_hi(d));
+      ls[x & 3] = ptx::add2(ls[x & 3], ptx::f2(e0, e1));
+      pk[x] = ptx::pack_bf16x2(e0, e1);
+    }
+  }
+};
+
+// Takes the row's maximum over a new tile's scores `top` into m: lazily, when it
+// has grown by more than kGrow, so that P stays below 2^8.  Then the row of O at
+// `to` (D columns) and the sum l are rescaled, once `o_ready` says that the
+// product that last wrote O is complete (false: that wait gave up, and so does
+// this).
+template <int D, class F>
+__device__ __forceinline__ bool take_max(float top, uint32_t to, float c, float& m, float& l, F o_ready) {
+  const float m_new = fmaxf(m, top);
   const bool grow = (m_new - m) * c > kGrow;  // false while the row has no key (NaN)
   const bool first = m == -INFINITY;
   if (__any_sync(0xffffffffu, grow && !first)) {
@@ -133,31 +145,14 @@ __device__ __forceinline__ bool softmax_tile(uint32_t ts, uint32_t to, int ra, i
     }
   }
   if (grow) m = m_new;
-  const float nm = m == -INFINITY ? 0.f : -m * c;
-  const uint64_t c2 = ptx::f2(c, c), nm2 = ptx::f2(nm, nm);
-  uint64_t ls[4] = {0, 0, 0, 0};
-#pragma unroll
-  for (int hf = 0; hf < 2; ++hf) {
-    // P rounded to bf16 for the product (2^-8 of each weight at most); l sums
-    // the unrounded weights
-    uint32_t pk[32];
-#pragma unroll
-    for (int x = 0; x < 32; ++x) {
-      const uint32_t* sp = &s[2 * hf + (x >> 4)][2 * (x & 15)];
-      const uint64_t d = ptx::fma2(ptx::f2(__uint_as_float(sp[0]), __uint_as_float(sp[1])), c2, nm2);
-      const float e0 = ptx::ex2(ptx::f2_lo(d)), e1 = ptx::ex2(ptx::f2_hi(d));
-      ls[x & 3] = ptx::add2(ls[x & 3], ptx::f2(e0, e1));
-      pk[x] = ptx::pack_bf16x2(e0, e1);
-    }
-    ptx::tmem_st32(ts + 32 * hf, pk);
-    ptx::tmem_wait_st();
-    ptx::tc_fence_before();
-    __syncwarp();
-    release(hf);
-  }
-  const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
-  l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
   return true;
+}
+
+// P written so far can be read by the tensor cores; then the warp together.
+__device__ __forceinline__ void p_written() {
+  ptx::tmem_wait_st();
+  ptx::tc_fence_before();
+  __syncwarp();
 }
 
 // One row of O at `to` over its sum l, into y (D columns) when `in`; `release`

@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       return true;
     };
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at(p, wi);
+      const Work w = work_at<kBN>(p, wi);
       const bool active = rank ? w.lo[1] < w.hi[1] : w.lo[0] < w.hi[0];
       if (active) {
         if (lane == 0) {
@@ -180,7 +180,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int base = 0, nq = 0, c = 0;  // first unit of the item, items, products so far
       bool ok = true, issued = false;
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at(p, wi);
+        const Work w = work_at<kBN>(p, wi);
         const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
         issued = true;
         nq += lo < hi;
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int base = 0, nq = 0, c = 0;
       bool ok = true, issued = false;
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at(p, wi);
+        const Work w = work_at<kBN>(p, wi);
         const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0], n = w.k_hi - w.k_lo;
         issued = true;
         nq += lo < hi;
@@ -267,11 +267,11 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- softmax and output ----------------
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t ts = tbase + lane_base, to = ts + kOCol;
+    const uint32_t to = tbase + lane_base + kOCol;
     int n = 0, no = 0;
     bool ok = true;
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at(p, wi);
+      const Work w = work_at<kBN>(p, wi);
       const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
       if (lo >= hi) continue;
       const int tok = w.tok0 + rank * tt + row / p.pk;
@@ -282,15 +282,31 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       for (int kt = lo; kt < hi; ++kt, ++n) {
         if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
         ptx::tc_fence_after();
-        ok = softmax_tile<D>(ts + (n & 1) * kBN, to, ra, rb, kt * kBN, p.c, m, l, [&] {
+        Scores<kBN> s;
+        const uint32_t ts = tbase + lane_base + (n & 1) * kBN;
+        s.load(ts);
+        s.mask(ra, rb, kt * kBN);
+        ok = take_max<D>(s.max(), to, p.c, m, l, [&] {
           const bool done =
               __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, lim));
           ptx::tc_fence_after();
           return done;
-        }, [&](int h) {
-          if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][h]);
         });
         if (!ok) break;
+        const float nm = m == -INFINITY ? 0.f : -m * p.c;
+        const uint64_t c2 = ptx::f2(p.c, p.c), nm2 = ptx::f2(nm, nm);
+        uint64_t ls[4] = {0, 0, 0, 0};
+        uint32_t pk[32];
+        s.weights<0, 64>(c2, nm2, ls, pk);
+        ptx::tmem_st32(ts, pk);
+        p_written();
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][0]);
+        s.weights<64, 64>(c2, nm2, ls, pk);
+        ptx::tmem_st32(ts + 32, pk);
+        p_written();
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][1]);
+        const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
+        l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
       }
       if (!ok || !(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.o_full, no & 1, abort, lim)))) break;
       ++no;
