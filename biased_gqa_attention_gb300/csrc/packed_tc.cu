@@ -54,6 +54,9 @@ struct Cfg {
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, KN, 0, 0);
   static_assert(kPCol + KN / 2 <= kOCol, "tensor memory columns");
+  // K units keep to the even slots and V units to the odd ones, so that the
+  // warps that read only the ones or the others see every phase of their slots
+  static_assert(kUnits % 2 == 0, "ring");
   static constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, D, 0, 1);
   static_assert(kSmem <= 232448 && kUnits >= 4, "shared memory");
 };

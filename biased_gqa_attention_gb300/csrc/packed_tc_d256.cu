@@ -1,18 +1,20 @@
 // packed_tc_d256.cu -- packed prefill on the 5th-generation tensor cores for
 // head size 256.
 //
-// Tensor memory holds S_0, S_1 (128 columns each) and one O (256 columns), so a
-// CTA has one M = 128 query tile; the scores of key tile j + 1 are computed
-// while tile j goes through the softmax.  A K and a V tile are 64 KB each for
-// 2240 tensor cycles: 58 bytes a cycle and SM from L2, about all it gives.  So
-// two CTAs form a cluster and take the two query tiles of one item (the same
-// keys): each loads half of every unit and multicasts it to both, which halves
-// the reads.
+// Tensor memory holds S, P (bf16) and one O of 256 columns, so a CTA has one
+// M = 128 query tile; QK(j + 1) is issued as soon as the softmax has S(j) in
+// registers.  A K and a V tile are 64 KB each for 2048 tensor cycles: 64 bytes a
+// cycle and SM from L2, about all it gives.  So two CTAs form a cluster and take
+// the two query tiles of one item (the same keys): each loads half of every unit
+// and multicasts it to both, which halves the reads.  What is left is shared
+// memory: Q and K as operands take all of its 128 bytes a cycle during QK, V
+// half of them during PV, and the tiles' writes come on top (2560 cycles for 2048
+// of tensor work).  Measured, 7644 tokens of 16 heads in three prompts, window
+// 1024: 107 us, 956 TFLOP/s of the attended pairs; units of 16 KB: 112 us.
 //   warp 0     loads: its Q tile; its half of each 32 KB unit of K (128 keys by
 //              128 columns) and V (64 keys by 256 columns)
-//   warps 1, 2 issue the MMAs, one Q K^T, the other P V (a thread's issue takes
-//              about as long as the tensor pipe's work: one warp for both left
-//              the pipe idle)
+//   warps 1, 2 issue the MMAs, one Q K^T, the other P V: neither stands in the
+//              other's waits
 //   warps 3-6  softmax and output, a query row per thread
 // A unit's slot is refilled when both CTAs' MMAs have read it (their commits
 // arrive in both CTAs).
@@ -29,32 +31,30 @@ using namespace packed;
 
 constexpr int D = 256;
 constexpr int kThreads = 224;
+constexpr int kParts = 2;  // units of a K or V tile
 constexpr int kUnits = 5;
 constexpr int kUnit = 32768;
+constexpr int kVKeys = kBN / kParts;  // keys of a V unit
 constexpr int kQBytes = kBM * D * 2;
 constexpr int kOffKV = kQBytes;
 constexpr int kOffBar = kOffKV + kUnits * kUnit;
 constexpr int kSmem = kOffBar + 512 + 1024;
-constexpr uint32_t kOCol = 256;
+constexpr uint32_t kPCol = 128, kOCol = 256;  // tensor memory: S, P, O
 constexpr uint32_t kIdescQK = ptx::idesc_bf16_f32(kBM, kBN, 0, 0);
 constexpr uint32_t kIdescPV = ptx::idesc_bf16_f32(kBM, D, 0, 1);
 constexpr uint16_t kBoth = 3;
 static_assert(kSmem <= 232448, "shared memory");
+static_assert(kParts == 2, "a part of P per V unit, two chunks per K unit");
 
 struct Bars {
   uint64_t q_full, q_empty;
   uint64_t u_full[kUnits], u_empty[kUnits], v_land[kUnits];
-  uint64_t s_full[2], p_full[2][2], pv_done[2];  // of each S; p_full of each half of its P
+  uint64_t s_full, s_free, p_full[2], pv_done;  // p_full: of each half of P
   uint64_t o_full, o_free, drain[2];
   uint32_t tmem_base;
   int abort;
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
-
-// Units leave in the order K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1},
-// two each: the first of K_j and of V_j.
-__device__ __forceinline__ int k_unit(int j) { return j == 0 ? 0 : 4 * j - 2; }
-__device__ __forceinline__ int v_unit(int j, int n) { return j == n - 1 ? 4 * n - 2 : 4 * j + 4; }
 
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     packed_tc_d256_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
@@ -74,15 +74,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     ptx::mbar_init(&bar.q_empty, 1);
     for (int u = 0; u < kUnits; ++u) {
       ptx::mbar_init(&bar.u_full[u], 1);
-      ptx::mbar_init(&bar.u_empty[u], 2);
+      ptx::mbar_init(&bar.u_empty[u], 4);  // two MMA warps of two CTAs
       ptx::mbar_init(&bar.v_land[u], 1);
     }
-    for (int s = 0; s < 2; ++s) {
-      ptx::mbar_init(&bar.s_full[s], 1);
-      ptx::mbar_init(&bar.p_full[s][0], 4);
-      ptx::mbar_init(&bar.p_full[s][1], 4);
-      ptx::mbar_init(&bar.pv_done[s], 1);
-    }
+    ptx::mbar_init(&bar.s_full, 1);
+    ptx::mbar_init(&bar.s_free, 4);
+    ptx::mbar_init(&bar.p_full[0], 4);
+    ptx::mbar_init(&bar.p_full[1], 4);
+    ptx::mbar_init(&bar.pv_done, 1);
     ptx::mbar_init(&bar.o_full, 1);
     ptx::mbar_init(&bar.o_free, 128);
     for (int s = 0; s < 2; ++s) ptx::mbar_init(&bar.drain[s], 1);
@@ -114,39 +113,33 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- loads ----------------
     int u = 0, nq = 0;
     bool ok = true;
-    // the next unit: its slot is free in both CTAs, the barrier is armed, this CTA's half on its way to both
-    auto load = [&](const CUtensorMap* map, bool tail, int32_t row, int32_t hk, int32_t chunk, int half_bytes) -> bool {
-      const int s = u % kUnits;
-      if (lane == 0) {
-        ok = u < kUnits || wait_or_abort(&bar.u_empty[s], ((u / kUnits) - 1) & 1, abort, lim);
-        if (ok) {
-          uint64_t* full = tail ? &bar.v_land[s] : &bar.u_full[s];
+    // A K or V tile: a lane per unit waits until the unit's slot is free in both
+    // CTAs, arms its barrier and sends this CTA's half to both.  (Issuing a
+    // request takes a lane some 500 cycles; lanes do it side by side.)
+    auto load = [&](bool is_v, const Work& w, int kt) -> bool {
+      bool sent = true;
+      if (lane < kParts) {
+        const int x = u + lane, s = x % kUnits, k0 = kt * kBN + (is_v ? lane * kVKeys : 0);
+        sent = x < kUnits || wait_or_abort(&bar.u_empty[s], ((x / kUnits) - 1) & 1, abort, lim);
+        if (sent) {
+          uint64_t* full = is_v && k0 + kVKeys > w.len ? &bar.v_land[s] : &bar.u_full[s];
           ptx::mbar_arrive_expect_tx(full, kUnit);
-          ptx::tma_load_4d_multicast(sKV + s * kUnit + rank * half_bytes, map, full, 0, row, hk, chunk, kBoth);
+          ptx::tma_load_4d_multicast(sKV + s * kUnit + rank * (kUnit / 2), is_v ? &vmap : &kmap, full, 0, w.row0 + k0, w.hk,
+                                     is_v ? 2 * rank : 2 * lane + rank, kBoth);
         }
       }
-      ok = __shfl_sync(0xffffffffu, ok, 0);
+      ok = __all_sync(0xffffffffu, sent);
+      armed = u + kParts;
       if (!ok) return false;
-      armed = u + 1;
-      return true;
-    };
-    auto load_k = [&](const Work& w, int kt) -> bool {
-      for (int part = 0; part < 2; ++part, ++u)  // 128 columns; this CTA's half is one 64-column chunk
-        if (!load(&kmap, false, w.row0 + kt * kBN, w.hk, 2 * part + rank, kUnit / 2)) return false;
-      return true;
-    };
-    auto load_v = [&](const Work& w, int kt) -> bool {
-      for (int part = 0; part < 2; ++part, ++u) {  // 64 keys; this CTA's half is two chunks
-        const int k0 = kt * kBN + part * 64, s = u % kUnits;
-        const bool tail = k0 + 64 > w.len;
-        if (!load(&vmap, tail, w.row0 + k0, w.hk, 2 * rank, kUnit / 2)) return false;
-        if (tail) {
-          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_land[s], (tails >> s) & 1, abort, lim)))) return false;
-          tails ^= 1u << s;
-          zero_rows<D>(sKV + s * kUnit, max(0, w.len - k0), 64, lane);
-          if (lane == 0) ptx::mbar_arrive(&bar.u_full[s]);
-        }
+      for (int part = 0; is_v && part < kParts; ++part) {
+        const int k0 = kt * kBN + part * kVKeys, s = (u + part) % kUnits;
+        if (k0 + kVKeys <= w.len) continue;
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_land[s], (tails >> s) & 1, abort, lim)))) return false;
+        tails ^= 1u << s;
+        zero_rows<D>(sKV + s * kUnit, max(0, w.len - k0), kVKeys, lane);
+        if (lane == 0) ptx::mbar_arrive(&bar.u_full[s]);
       }
+      u += kParts;
       return true;
     };
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
@@ -164,102 +157,81 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         if (!ok) break;
         ++nq;
       }
-      if (!load_k(w, w.k_lo)) break;
+      if (!load(false, w, w.k_lo)) break;
       for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
-        if (kt + 1 < w.k_hi && !load_k(w, kt + 1)) break;
-        load_v(w, kt);
+        if (kt + 1 < w.k_hi && !load(false, w, kt + 1)) break;
+        load(true, w, kt);
       }
     }
     if (lane == 0 && *abort && nq) ptx::mbar_wait_bounded(&bar.q_full, (nq - 1) & 1, kWaitPolls >> 6);
     __syncwarp();
-  } else if (warp == 1) {
-    // ---------------- Q K^T ----------------
+  } else if (warp < 3) {
+    // ---------------- MMAs: Q K^T (warp 1), P V (warp 2) ----------------
+    // Both warps walk over all units in the order they are loaded, and a slot is
+    // free when both of both CTAs have passed it: K and V units share the slots,
+    // and a wait for one phase of a slot's barrier is sound only for a thread
+    // that has seen the phase before it and cannot miss the one after.
     if (lane == 0) {
+      const bool pv = warp == 2;
       const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
       const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
-      int base = 0, nq = 0, c = 0;  // first unit of the item, items, products so far
-      bool ok = true, issued = false;
-      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at<kBN>(p, wi);
-        const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
-        issued = true;
-        nq += lo < hi;
-        for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
-          const int u = base + k_unit(kt - w.k_lo);
-          const bool active = kt >= lo && kt < hi;
-          if (active) {
-            if (kt == lo && !(ok = wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim))) break;
-            // the P that lay in this S has been read
-            if (c > 1 && !(ok = wait_or_abort(&bar.pv_done[c & 1], ((c >> 1) - 1) & 1, abort, lim))) break;
-          }
-          for (int part = 0; part < 2; ++part) {
-            const int s = (u + part) % kUnits;
-            if (!(ok = wait_or_abort(&bar.u_full[s], ((u + part) / kUnits) & 1, abort, lim))) break;
-            ptx::tc_fence_after();
-            if (active) {
-              const uint64_t kd = kdesc + ((s * kUnit) >> 4);
-#pragma unroll
-              for (int k = 0; k < 8; ++k) {
-                const uint64_t qd = qdesc + (((2 * part + (k >> 2)) * (kBM * 128) + (k & 3) * 32) >> 4);
-                ptx::umma_bf16(tbase + (c & 1) * kBN, qd, kd + (((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4), kIdescQK,
-                               part > 0 || k > 0);
-              }
-              if (part == 1) ptx::umma_commit(&bar.s_full[c & 1]);
-            }
-            ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
-          }
-          if (!ok) break;
-          c += active;
-          if (kt == hi - 1) ptx::umma_commit(&bar.q_empty);
-        }
-        base += 4 * (w.k_hi - w.k_lo);
-      }
-      // every MMA issued has completed before tensor memory is released
-      if (issued) {
-        ptx::umma_commit(&bar.drain[0]);
-        if (!ptx::mbar_wait_bounded(&bar.drain[0], 0, kWaitPolls)) *abort = 1;
-      }
-    }
-    __syncwarp();
-  } else if (warp == 2) {
-    // ---------------- P V ----------------
-    if (lane == 0) {
-      const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 64 * 128, 1024);
-      int base = 0, nq = 0, c = 0;
+      const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kVKeys * 128, 1024);
+      int u = 0, nq = 0, c = 0;  // units, items, products so far
       bool ok = true, issued = false;
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at<kBN>(p, wi);
         const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0], n = w.k_hi - w.k_lo;
         issued = true;
         nq += lo < hi;
-        for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
-          const int u = base + v_unit(kt - w.k_lo, n);
-          const bool active = kt >= lo && kt < hi, first = kt == lo;
-          if (active && first && nq > 1 && !(ok = wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim))) break;
-          for (int part = 0; part < 2; ++part) {
-            const int s = (u + part) % kUnits;
-            if (!(ok = wait_or_abort(&bar.u_full[s], ((u + part) / kUnits) & 1, abort, lim))) break;
-            if (active) {
-              if (!(ok = wait_or_abort(&bar.p_full[c & 1][part], (c >> 1) & 1, abort, lim))) break;
+        // K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1}
+        for (int i = 0; i < 2 * n && ok; ++i) {
+          const bool last = i == 2 * n - 1, is_v = last || (i > 0 && i % 2 == 0);
+          const int kt = w.k_lo + (last ? n - 1 : is_v ? i / 2 - 1 : (i + 1) / 2);
+          const bool mine = is_v == pv && kt >= lo && kt < hi, first = kt == lo;
+          if (mine && !pv) {
+            if (first && !(ok = wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim))) break;
+            // the scores before these are in the softmax's registers
+            if (c > 0 && !(ok = wait_or_abort(&bar.s_free, (c - 1) & 1, abort, lim))) break;
+          } else if (mine) {
+            if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim))) break;
+          }
+          for (int part = 0; part < kParts; ++part, ++u) {
+            const int s = u % kUnits;
+            if (!(ok = wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim))) break;
+            if (mine && !pv) {
+              ptx::tc_fence_after();
+              const uint64_t kd = kdesc + ((s * kUnit) >> 4), qd = qdesc + ((part * 2 * (kBM * 128)) >> 4);
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const uint32_t off = ((k >> 2) * (kBN * 128) + (k & 3) * 32) >> 4;
+                ptx::umma_bf16(tbase, qd + off, kd + off, kIdescQK, part > 0 || k > 0);
+              }
+              if (part == 1) {
+                ptx::umma_commit(&bar.s_full);
+                if (kt == hi - 1) ptx::umma_commit(&bar.q_empty);
+              }
+            } else if (mine) {
+              if (!(ok = wait_or_abort(&bar.p_full[part], c & 1, abort, lim))) break;
               ptx::tc_fence_after();
               const uint64_t vd = vdesc + ((s * kUnit) >> 4);
 #pragma unroll
-              for (int k = 0; k < 4; ++k)
-                ptx::umma_bf16_ts(tbase + kOCol, tbase + (c & 1) * kBN + (part * 4 + k) * 8, vd + ((k * 2048) >> 4),
+              for (int k = 0; k < kVKeys / 16; ++k)
+                ptx::umma_bf16_ts(tbase + kOCol, tbase + kPCol + (part * (kVKeys / 16) + k) * 8, vd + ((k * 2048) >> 4),
                                   kIdescPV, !first || part > 0 || k > 0);
-              if (part == 1) ptx::umma_commit(&bar.pv_done[c & 1]);
+              if (part == 1) {
+                ptx::umma_commit(&bar.pv_done);
+                if (kt == hi - 1) ptx::umma_commit(&bar.o_full);
+              }
             }
             ptx::umma_commit_multicast(&bar.u_empty[s], kBoth);
           }
-          if (!ok) break;
-          c += active;
-          if (kt == hi - 1) ptx::umma_commit(&bar.o_full);
+          c += mine;
         }
-        base += 4 * n;
       }
+      // every MMA issued has completed before tensor memory is released
       if (issued) {
-        ptx::umma_commit(&bar.drain[1]);
-        if (!ptx::mbar_wait_bounded(&bar.drain[1], 0, kWaitPolls)) *abort = 1;
+        ptx::umma_commit(&bar.drain[warp - 1]);
+        if (!ptx::mbar_wait_bounded(&bar.drain[warp - 1], 0, kWaitPolls)) *abort = 1;
       }
     }
     __syncwarp();
@@ -267,7 +239,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     // ---------------- softmax and output ----------------
     const int row = 32 * (warp & 3) + lane;
     const uint32_t lane_base = static_cast<uint32_t>(32 * (warp & 3)) << 16;
-    const uint32_t to = tbase + lane_base + kOCol;
+    const uint32_t ts = tbase + lane_base, tp = ts + kPCol, to = ts + kOCol;
     int n = 0, no = 0;
     bool ok = true;
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
@@ -280,31 +252,37 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       if (!valid) ra = rb = 0;
       float m = -INFINITY, l = 0.f;
       for (int kt = lo; kt < hi; ++kt, ++n) {
-        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[n & 1], (n >> 1) & 1, abort, lim)))) break;
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full, n & 1, abort, lim)))) break;
         ptx::tc_fence_after();
         Scores<kBN> s;
-        const uint32_t ts = tbase + lane_base + (n & 1) * kBN;
         s.load(ts);
+        ptx::tc_fence_before();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&bar.s_free);
         s.mask(ra, rb, kt * kBN);
-        ok = take_max<D>(s.max(), to, p.c, m, l, [&] {
-          const bool done =
-              __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done[(n - 1) & 1], ((n - 1) >> 1) & 1, abort, lim));
-          ptx::tc_fence_after();
-          return done;
-        });
-        if (!ok) break;
+        // PV(n - 1) is complete: P may be written, O rescaled
+        bool p_free = n == 0;
+        auto pv_complete = [&] {
+          if (!p_free) {
+            p_free = __all_sync(0xffffffffu, wait_or_abort(&bar.pv_done, (n - 1) & 1, abort, lim));
+            ptx::tc_fence_after();
+          }
+          return p_free;
+        };
+        if (!(ok = take_max<D>(s.max(), to, p.c, m, l, pv_complete))) break;
         const float nm = m == -INFINITY ? 0.f : -m * p.c;
         const uint64_t c2 = ptx::f2(p.c, p.c), nm2 = ptx::f2(nm, nm);
         uint64_t ls[4] = {0, 0, 0, 0};
         uint32_t pk[32];
         s.weights<0, 64>(c2, nm2, ls, pk);
-        ptx::tmem_st32(ts, pk);
+        if (!(ok = pv_complete())) break;
+        ptx::tmem_st32(tp, pk);
         p_written();
-        if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][0]);
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[0]);
         s.weights<64, 64>(c2, nm2, ls, pk);
-        ptx::tmem_st32(ts + 32, pk);
+        ptx::tmem_st32(tp + 32, pk);
         p_written();
-        if (lane == 0) ptx::mbar_arrive(&bar.p_full[n & 1][1]);
+        if (lane == 0) ptx::mbar_arrive(&bar.p_full[1]);
         const uint64_t sum = ptx::add2(ptx::add2(ls[0], ls[1]), ptx::add2(ls[2], ls[3]));
         l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
       }
@@ -351,7 +329,7 @@ cudaError_t launch_packed_tc_d256(const PackedParams& p, cudaStream_t s) {
   const uint64_t k_dims[4] = {64, T, static_cast<uint64_t>(p.Hkv), chunks};
   const uint64_t k_str[3] = {static_cast<uint64_t>(p.k_stride) * 2, D * 2, 128};
   const uint64_t v_str[3] = {static_cast<uint64_t>(p.v_stride) * 2, D * 2, 128};
-  const uint32_t k_box[4] = {64, kBN, 1, 1}, v_box[4] = {64, 64, 1, 2};
+  const uint32_t k_box[4] = {64, kBN, 1, 1}, v_box[4] = {64, kVKeys, 1, 2};
   if (!make_tensor_map_bf16(&qmap, p.q, 4, q_dims, q_str, q_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&kmap, p.k, 4, k_dims, k_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&vmap, p.v, 4, k_dims, v_str, v_box, CU_TENSOR_MAP_SWIZZLE_128B))

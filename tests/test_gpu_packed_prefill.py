@@ -224,3 +224,21 @@ def test_a_wait_that_runs_out_is_reported(D):
     y = run(q, k, v, cu, 0.1, True, 0)
     ref, tol = reference(q, k, v, cu, 0.1, True, 0)
     check(y, ref, tol, "after")
+
+
+@pytest.mark.parametrize("D,window", [(256, 90), (256, 0), (128, 90), (64, 0)])
+def test_the_same_bits_from_cold_and_warm_caches(D, window):
+    """Copies that land late, early and in other orders (L2 full of other data, or
+    of this) change no bit."""
+    lens = (1, 300, 129, 700, 64, 257)
+    q, k, v, cu = make(lens, 8, 4, D, torch.bfloat16, True)
+    other = torch.empty(1 << 26, dtype=torch.float32, device="cuda")  # twice the L2
+    good = run(q, k, v, cu, 1.0 / math.sqrt(D), True, window)
+    ref, tol = reference(q, k, v, cu, 1.0 / math.sqrt(D), True, window)
+    check(good, ref, tol, "y")
+    for i in range(60):
+        if i % 3:
+            other.fill_(float(i))
+        if i % 3 == 2:
+            k.sum()  # K warm, V cold
+        assert torch.equal(run(q, k, v, cu, 1.0 / math.sqrt(D), True, window), good), i
