@@ -9,15 +9,18 @@
 // and multicasts it to both, which halves the reads.  What is left is shared
 // memory: Q and K as operands take all of its 128 bytes a cycle during QK, V
 // half of them during PV, and the tiles' writes come on top (2560 cycles for 2048
-// of tensor work).  Measured, 7644 tokens of 16 heads in three prompts, window
-// 1024: 107 us, 956 TFLOP/s of the attended pairs; units of 16 KB: 112 us.
+// of tensor work).
 //   warp 0     loads: its Q tile; its half of each 32 KB unit of K (128 keys by
 //              128 columns) and V (64 keys by 256 columns)
 //   warps 1, 2 issue the MMAs, one Q K^T, the other P V: neither stands in the
 //              other's waits
 //   warps 3-6  softmax and output, a query row per thread
 // A unit's slot is refilled when both CTAs' MMAs have read it (their commits
-// arrive in both CTAs).
+// arrive in both CTAs).  K has a ring of two units and V one of three: with the
+// 3 and 2 the other way round, 107 us on the case below; with one ring for both,
+// which each MMA warp then has to walk whole, 116 us; with units of 16 KB, 112 us.
+// Measured, 7644 tokens of 16 heads in three prompts, window 1024: 105 us, 978
+// TFLOP/s of the attended pairs.
 #include "internal.h"
 #include "packed_tc.cuh"
 #include "packed_tc.h"
@@ -32,7 +35,7 @@ using namespace packed;
 constexpr int D = 256;
 constexpr int kThreads = 224;
 constexpr int kParts = 2;  // units of a K or V tile
-constexpr int kUnits = 5;
+constexpr int kKUnits = 2, kVUnits = 3, kUnits = kKUnits + kVUnits;  // rings of K and of V, one behind the other
 constexpr int kUnit = 32768;
 constexpr int kVKeys = kBN / kParts;  // keys of a V unit
 constexpr int kQBytes = kBM * D * 2;
@@ -56,6 +59,10 @@ struct Bars {
 };
 static_assert(sizeof(Bars) <= 512, "barrier block");
 
+// Slot and round of the x-th unit of K or of V.
+__device__ __forceinline__ int slot(bool is_v, int x) { return is_v ? kKUnits + x % kVUnits : x % kKUnits; }
+__device__ __forceinline__ int round(bool is_v, int x) { return is_v ? x / kVUnits : x / kKUnits; }
+
 __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     packed_tc_d256_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                           const __grid_constant__ CUtensorMap vmap, const PackedParams p) {
@@ -74,7 +81,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     ptx::mbar_init(&bar.q_empty, 1);
     for (int u = 0; u < kUnits; ++u) {
       ptx::mbar_init(&bar.u_full[u], 1);
-      ptx::mbar_init(&bar.u_empty[u], 4);  // two MMA warps of two CTAs
+      ptx::mbar_init(&bar.u_empty[u], 2);  // an MMA warp of each CTA
       ptx::mbar_init(&bar.v_land[u], 1);
     }
     ptx::mbar_init(&bar.s_full, 1);
@@ -106,12 +113,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
   const int tt = p.tile_tok / 2;
   Rounds rounds(n_work, blockIdx.x / 2, gridDim.x / 2);
-  int armed = 0;       // warp 0: units whose barriers expect bytes
+  int armed[2] = {0, 0};  // warp 0: units whose barriers expect bytes
   uint32_t tails = 0;  // warp 0: phase of each unit's v_land
 
   if (warp == 0) {
     // ---------------- loads ----------------
-    int u = 0, nq = 0;
+    int nu[2] = {0, 0}, nq = 0;  // units of K and of V, items so far
     bool ok = true;
     // A K or V tile: a lane per unit waits until the unit's slot is free in both
     // CTAs, arms its barrier and sends this CTA's half to both.  (Issuing a
@@ -119,8 +126,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     auto load = [&](bool is_v, const Work& w, int kt) -> bool {
       bool sent = true;
       if (lane < kParts) {
-        const int x = u + lane, s = x % kUnits, k0 = kt * kBN + (is_v ? lane * kVKeys : 0);
-        sent = x < kUnits || wait_or_abort(&bar.u_empty[s], ((x / kUnits) - 1) & 1, abort, lim);
+        const int x = nu[is_v] + lane, s = slot(is_v, x), r = round(is_v, x), k0 = kt * kBN + (is_v ? lane * kVKeys : 0);
+        sent = r == 0 || wait_or_abort(&bar.u_empty[s], (r - 1) & 1, abort, lim);
         if (sent) {
           uint64_t* full = is_v && k0 + kVKeys > w.len ? &bar.v_land[s] : &bar.u_full[s];
           ptx::mbar_arrive_expect_tx(full, kUnit);
@@ -129,17 +136,17 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         }
       }
       ok = __all_sync(0xffffffffu, sent);
-      armed = u + kParts;
+      armed[is_v] = nu[is_v] + kParts;
       if (!ok) return false;
       for (int part = 0; is_v && part < kParts; ++part) {
-        const int k0 = kt * kBN + part * kVKeys, s = (u + part) % kUnits;
+        const int k0 = kt * kBN + part * kVKeys, s = slot(true, nu[1] + part);
         if (k0 + kVKeys <= w.len) continue;
         if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_land[s], (tails >> s) & 1, abort, lim)))) return false;
         tails ^= 1u << s;
         zero_rows<D>(sKV + s * kUnit, max(0, w.len - k0), kVKeys, lane);
         if (lane == 0) ptx::mbar_arrive(&bar.u_full[s]);
       }
-      u += kParts;
+      nu[is_v] += kParts;
       return true;
     };
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
@@ -167,27 +174,23 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     __syncwarp();
   } else if (warp < 3) {
     // ---------------- MMAs: Q K^T (warp 1), P V (warp 2) ----------------
-    // Both warps walk over all units in the order they are loaded, and a slot is
-    // free when both of both CTAs have passed it: K and V units share the slots,
-    // and a wait for one phase of a slot's barrier is sound only for a thread
-    // that has seen the phase before it and cannot miss the one after.
+    // (K and V have rings of their own, so that each warp sees every phase of its
+    // slots: a wait for one phase of a barrier passes while the phase before it is
+    // still open.)
     if (lane == 0) {
       const bool pv = warp == 2;
       const uint64_t qdesc = ptx::smem_desc_sw128(ptx::smem_u32(sm), 16, 1024);
       const uint64_t kdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), 16, 1024);
       const uint64_t vdesc = ptx::smem_desc_sw128(ptx::smem_u32(sKV), kVKeys * 128, 1024);
-      int u = 0, nq = 0, c = 0;  // units, items, products so far
+      int u = 0, nq = 0, c = 0;  // units of its kind, items, products so far
       bool ok = true, issued = false;
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
         const Work w = work_at<kBN>(p, wi);
-        const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0], n = w.k_hi - w.k_lo;
+        const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
         issued = true;
         nq += lo < hi;
-        // K_0, K_1, V_0, K_2, V_1, ..., K_{n-1}, V_{n-2}, V_{n-1}
-        for (int i = 0; i < 2 * n && ok; ++i) {
-          const bool last = i == 2 * n - 1, is_v = last || (i > 0 && i % 2 == 0);
-          const int kt = w.k_lo + (last ? n - 1 : is_v ? i / 2 - 1 : (i + 1) / 2);
-          const bool mine = is_v == pv && kt >= lo && kt < hi, first = kt == lo;
+        for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt) {
+          const bool mine = kt >= lo && kt < hi, first = kt == lo;
           if (mine && !pv) {
             if (first && !(ok = wait_or_abort(&bar.q_full, (nq - 1) & 1, abort, lim))) break;
             // the scores before these are in the softmax's registers
@@ -196,8 +199,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
             if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free, (nq - 2) & 1, abort, lim))) break;
           }
           for (int part = 0; part < kParts; ++part, ++u) {
-            const int s = u % kUnits;
-            if (!(ok = wait_or_abort(&bar.u_full[s], (u / kUnits) & 1, abort, lim))) break;
+            const int s = slot(pv, u);
+            if (!(ok = wait_or_abort(&bar.u_full[s], round(pv, u) & 1, abort, lim))) break;
             if (mine && !pv) {
               ptx::tc_fence_after();
               const uint64_t kd = kdesc + ((s * kUnit) >> 4), qd = qdesc + ((part * 2 * (kBM * 128)) >> 4);
@@ -305,10 +308,12 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   // what this CTA's barriers were armed for lands or was never sent.
   ptx::cluster_sync();
   if (warp == 0 && lane == 0 && *abort) {
-    for (int x = armed > kUnits ? armed - kUnits : 0; x < armed; ++x) {
-      ptx::mbar_wait_bounded(&bar.u_full[x % kUnits], (x / kUnits) & 1, kWaitPolls >> 6);
-      ptx::mbar_wait_bounded(&bar.v_land[x % kUnits], (tails >> (x % kUnits)) & 1, kWaitPolls >> 8);
-    }
+    for (int is_v = 0; is_v < 2; ++is_v)
+      for (int x = max(0, armed[is_v] - (is_v ? kVUnits : kKUnits)); x < armed[is_v]; ++x) {
+        const int s = slot(is_v, x);
+        ptx::mbar_wait_bounded(&bar.u_full[s], round(is_v, x) & 1, kWaitPolls >> 6);
+        ptx::mbar_wait_bounded(&bar.v_land[s], (tails >> s) & 1, kWaitPolls >> 8);
+      }
   }
   __syncwarp();
   ptx::cluster_sync();
