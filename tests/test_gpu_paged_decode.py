@@ -317,3 +317,18 @@ def test_a_wait_that_runs_out_is_reported():
     y = run(q, k, v, table, nonpad, 0.1, 0)
     ref, tol = reference(q, k, v, table, lens, 0, 0.1)
     check(y, ref, tol, "after")
+
+
+@pytest.mark.parametrize("D,g,page", [(64, 4, 16), (128, 2, 64), (128, 16, 16), (256, 2, 32), (512, 8, 16), (128, 3, 7), (96, 2, 16)])
+def test_the_same_bits_from_cold_and_warm_caches(D, g, page):
+    """Copies that land late, early and in other orders change no bit."""
+    lens = (4000, 17, 900, 0, 2500, 333)
+    q, k, v, table, nonpad = make(lens, 2 * g, 2, D, page, torch.bfloat16)
+    other = torch.empty(1 << 26, dtype=torch.float32, device="cuda")  # twice the L2
+    good = run(q, k, v, table, nonpad, 1.0 / math.sqrt(D), 0)
+    for i in range(60):
+        if i % 3:
+            other.fill_(float(i))
+        if i % 3 == 2:
+            k.sum()  # K warm, V cold
+        assert torch.equal(run(q, k, v, table, nonpad, 1.0 / math.sqrt(D), 0), good), i
