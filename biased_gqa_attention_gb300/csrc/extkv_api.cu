@@ -57,6 +57,8 @@ void note_launches(int n) { g_launches = n; }
 
 uint32_t wait_limit_setting() { return g_wait_limit_plus1; }
 
+int algo_setting() { return g_algo; }
+
 void note_last_call(const char* name) {
   g_last_kernel = name;
   g_last_launches = g_launches;

@@ -94,6 +94,9 @@ void note_launches(int n);
 // The calling thread's extkv_set_wait_polls() setting, as AttnArgs::wait_limit_plus1.
 uint32_t wait_limit_setting();
 
+// The calling thread's extkv_set_algo() setting.
+int algo_setting();
+
 // The poll limit of a pipeline wait for a call's wait_limit_plus1.
 inline uint32_t wait_limit(uint32_t plus1, uint32_t own) { return plus1 ? plus1 - 1 : own; }
 

@@ -6,6 +6,7 @@
 #include <stdint.h>
 
 #include "extkv.h"
+#include "internal.h"
 
 namespace extkv {
 
@@ -50,8 +51,10 @@ struct PagedDecodeArgs {
   int32_t* status;
   cudaStream_t stream;
   uint32_t wait_limit_plus1;  // as AttnArgs
+  int variant;                // kDecodeAuto, kDecodeStreamK (the axis of tiles) or kDecodeCluster
 };
 size_t paged_decode_workspace_bytes(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype);
+// cudaErrorNotSupported: the cluster kernel was asked for and cannot take the call.
 cudaError_t launch_paged_decode(const PagedDecodeArgs& a, const char** name);
 
 struct PackedArgs {

@@ -229,10 +229,15 @@ int attention_paged_decode(void* y, const void* q, const void* k_pages, const vo
   if (int rc = check_workspace(who, workspace, ws_bytes, paged_decode_workspace_bytes(B, Hq, Hkv, D, dtype))) return rc;
   PagedDecodeArgs a{y,      q,         k_pages,   v_pages,  page_table, nonpad,    scale,  window, B, Hq, Hkv, D,
                     num_pages, page_size, max_pages, q_stride, dtype,      workspace, status, static_cast<cudaStream_t>(stream),
-                    wait_limit_setting()};
+                    wait_limit_setting(),
+                    algo_setting() == EXTKV_ALGO_DECODE_STREAMK   ? kDecodeStreamK
+                    : algo_setting() == EXTKV_ALGO_DECODE_CLUSTER ? kDecodeCluster
+                                                                  : kDecodeAuto};
   const char* name = "";
   note_launches(0);
   const cudaError_t e = launch_paged_decode(a, &name);
+  if (e == cudaErrorNotSupported)
+    return fail(EXTKV_ERR_UNSUPPORTED, "%s: the cluster kernel cannot run this shape/type", who);
   if (e != cudaSuccess) return cuda_fail(e, "attention_paged_decode launch");
   note_last_call(name);
   return EXTKV_OK;

@@ -18,6 +18,7 @@
 // on timing.
 #include <algorithm>
 #include <cstring>
+#include <mutex>
 
 #include "common.cuh"
 #include "internal.h"
@@ -31,6 +32,7 @@ namespace extkv {
 namespace {
 
 constexpr uint32_t kWaitPolls = 1u << 22;  // bounded waits
+constexpr int kMaxCluster = 8;
 
 struct PagedParams {
   void* y;
@@ -43,6 +45,7 @@ struct PagedParams {
   int window, B, Hq, Hkv, g, D, page_size, max_pages;
   int64_t num_pages, q_stride;
   int box;     // rows of a TMA request
+  int cluster; // CTAs of a unit's cluster (cluster kernel)
   uint32_t wait_limit;
   int rows;    // query heads per unit (the kernel's row capacity)
   int groups;  // units per (sequence, KV head)
@@ -276,14 +279,20 @@ __device__ __forceinline__ void cp_async_wait() {
 //   else  any other page size: the consumer's lanes copy 16 bytes each
 //         (cp.async), a row's address from the page table.
 
-template <int D_, int NT_, int KT_, int SLOTS_, int WARPS_, bool TMA_>
+// Few short units (a small batch, a sliding window) leave the joining of CTAs as
+// a good part of the call.  There a cluster of CTAs takes one unit, each CTA an
+// equal share of its tiles, and the shares are joined through distributed shared
+// memory in rank order: one launch, no scan of the batch, no workspace.
+
+template <int D_, int NT_, int KT_, int SLOTS_, int WARPS_, bool TMA_, bool CLUSTER_ = false>
 struct MmaCfg {
   static constexpr int D = D_, NT = NT_, KT = KT_, SLOTS = SLOTS_, WARPS = WARPS_;
-  static constexpr bool TMA = TMA_;
+  static constexpr bool TMA = TMA_, CLUSTER = CLUSTER_;
   static constexpr int kThreads = (WARPS + (TMA ? 1 : 0)) * 32;
   static constexpr int kTile = KT * D * 2;  // a slot
   static constexpr int kRing = SLOTS * kTile;
-  static constexpr int kSmem = WARPS * kRing + 1024;
+  static constexpr int kShare = CLUSTER ? 8 * NT * (D * 4 + 8) : 0;  // a CTA's joined partial
+  static constexpr int kSmem = WARPS * kRing + kShare + 1024;
 };
 
 // What a warp leaves to its CTA: the units its part begins [0] and ends [1] in,
@@ -357,32 +366,49 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   }
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
+  const int cta = blockIdx.x;
+  Cursor<KT> cur{};
+  int n, mine = C::TMA && warp == W ? min(lane, W - 1) : warp;  // a consumer's part; the producer's lanes serve one each
+  int unit_tiles = 0, tiles_here = 0, rank = 0;
+  if constexpr (C::CLUSTER) {
+    __syncthreads();  // the barriers
+    rank = static_cast<int>(ptx::cluster_ctarank());
+    const int unit = cta / p.cluster;
+    cur.b = unit / p.units;
+    cur.u = unit - cur.b * p.units;
+    const int64_t np = p.nonpad[cur.b];
+    if (tid == 0 && rank == 0 && cur.u == 0 && (np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size))
+      report(p.status, EXTKV_DEV_BAD_NONPAD);
+    cur.keys = live_keys(p, cur.b);
+    cur.tiles = unit_tiles = tiles_of<KT>(cur.keys);
+    const int t0 = static_cast<int>(static_cast<int64_t>(unit_tiles) * rank / p.cluster);
+    tiles_here = static_cast<int>(static_cast<int64_t>(unit_tiles) * (rank + 1) / p.cluster) - t0;
+    auto first_of = [&](int w) { return static_cast<int>(static_cast<int64_t>(tiles_here) * w / W); };
+    cur.t = t0 + first_of(mine);
+    n = first_of(mine + 1) - first_of(mine);
+  } else {
   const bool few = p.B <= 32;
   const LaneScan<KT> scan(p);  // (of the first 32 sequences where there are more: not used)
   int per = 0;
   if (few) __syncthreads();  // the barriers
   else per = scan_tiles<KT>(p, pre, warp_sum);
   const Axis axis(p, few ? scan.total(p) : pre[blockDim.x] * p.units);
-  const int cta = blockIdx.x;
   if (cta >= axis.n) return;
   const int64_t c0 = axis.start(cta);
-  const int tiles_here = static_cast<int>(axis.start(cta + 1) - c0);  // at least one
+  tiles_here = static_cast<int>(axis.start(cta + 1) - c0);  // at least one
   auto first_of = [&](int w) { return static_cast<int>(static_cast<int64_t>(tiles_here) * w / W); };
   auto at_tile = [&](int64_t f) { return few ? scan.cursor_at(p, f) : cursor_at<KT>(p, pre, per, f); };
-  // a consumer's part; the producer's lanes serve a consumer each
-  Cursor<KT> cur{};
-  int mine = warp;
   if (!C::TMA || warp < W) {
     if (first_of(mine) < first_of(mine + 1)) cur = at_tile(c0 + first_of(mine));
   } else {
-    mine = min(lane, W - 1);
     for (int w = 0; w < W; ++w)
       if (first_of(w) < first_of(w + 1)) {
         const Cursor<KT> c = at_tile(c0 + first_of(w));
         if (w == mine) cur = c;
       }
   }
-  const int n = first_of(mine + 1) - first_of(mine);
+  n = first_of(mine + 1) - first_of(mine);
+  }
 
   if (C::TMA && warp == W) {
     // ---------------- producer ----------------
@@ -750,10 +776,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 
   // ---- the units split over this CTA's warps (and maybe its neighbours)
   __syncthreads();
-  if (C::TMA && *abort) {  // nothing to join: a part is missing
-    if (tid == 0) report(p.status, EXTKV_DEV_TIMEOUT);
-    return;
-  }
+  const bool dead = C::TMA && *abort;  // nothing to join: a part is missing
+  if (dead && tid == 0) report(p.status, EXTKV_DEV_TIMEOUT);
+  if (!C::CLUSTER && dead) return;
+  float* share = reinterpret_cast<float*>(smem + W * C::kRing);  // cluster: this CTA's rows, then their (max, sum)
+  float2* share_ml = reinterpret_cast<float2*>(share + kRowsU * D);
   if (warp == 0) {
     // lane k looks at warp k's part; a unit's warps are neighbours, so the
     // members of a chain are the late partials of its unit and the early one
@@ -767,7 +794,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int64_t next_head = __shfl_sync(0xffffffffu, head, behind ? __ffs(behind) - 1 : 0);
     const bool late = some && r.late, early = some && r.early;
     const bool ends_late = late && !(behind && next_head == last);
-    const int64_t first = __shfl_sync(0xffffffffu, head, __ffs(busy) - 1);
+    const int64_t first = __shfl_sync(0xffffffffu, head, busy ? __ffs(busy) - 1 : 0);
     int c = 0;
     for (int w = 0; w < W; ++w)
 #pragma unroll
@@ -835,12 +862,59 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         uint2* y = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) +
                                             (static_cast<int64_t>(x.b) * p.Hq + hk * p.g + gr * kRowsU + r) * D);
         y[c4] = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+      } else if constexpr (C::CLUSTER) {
+        if (c4 == 0) share_ml[r] = make_float2(M, L);
+        reinterpret_cast<float4*>(share + r * D)[c4] = acc;
       } else {
         const int64_t at = (static_cast<int64_t>(cta) * 2 + x.slot) * kRowsU + r;
         if (c4 == 0) p.ml[at] = make_float2(M, L);
         reinterpret_cast<float4*>(p.part + at * D)[c4] = acc;
       }
     }
+  }
+  if constexpr (C::CLUSTER) {
+    const int unit = cta / p.cluster, b = unit / p.units, u = unit - b * p.units;
+    const int hk = u / p.groups, gr = u - hk * p.groups, heads = min(kRowsU, p.g - gr * kRowsU);
+    if (tiles_here == 0 && tid < kRowsU) share_ml[tid] = make_float2(-INFINITY, 0.f);
+    __syncthreads();
+    ptx::cluster_sync();
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+    if (unit_tiles != 1 && !dead) {  // one tile: a warp has written the rows
+      for (int i = rank * C::kThreads + tid; i < heads * (D / 4); i += p.cluster * C::kThreads) {
+        const int r = i / (D / 4), c4 = i - r * (D / 4);
+        float2 ml[kMaxCluster];
+        float4 v[kMaxCluster];
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          ml[k] = make_float2(-INFINITY, 0.f);
+          v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (k < p.cluster) {
+            const uint32_t at = ptx::map_cluster(share_ml + r, k);
+            ml[k] = make_float2(ptx::ld_cluster_f32(at), ptx::ld_cluster_f32(at + 4));
+            if (!(ml[k].x == -INFINITY && ml[k].y == 0.f)) v[k] = ptx::ld_cluster_f32x4(ptx::map_cluster(share + r * D + 4 * c4, k));
+          }
+        }
+        float M = -INFINITY, L = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) M = fmaxf(M, ml[k].x);
+        const float ref = M == -INFINITY ? 0.f : M;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kMaxCluster; ++k) {
+          const float wt = ml[k].x == -INFINITY ? 0.f : ptx::ex2(ml[k].x - ref);
+          L = fmaf(wt, ml[k].y, L);
+          acc.x = fmaf(wt, v[k].x, acc.x);
+          acc.y = fmaf(wt, v[k].y, acc.y);
+          acc.z = fmaf(wt, v[k].z, acc.z);
+          acc.w = fmaf(wt, v[k].w, acc.w);
+        }
+        const float inv = L != 0.f ? 1.f / L : 0.f;  // no key: a zero row
+        reinterpret_cast<uint2*>(y + static_cast<int64_t>(r) * D)[c4] =
+            make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+      }
+    }
+    __syncwarp();
+    ptx::cluster_sync();  // a CTA's share stays until its peers have read it
   }
 }
 
@@ -1128,6 +1202,73 @@ Plan plan_of(int64_t B, int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   return pl;
 }
 
+// The launch configuration of a cluster kernel.
+struct ClusterLaunch {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[2];
+  ClusterLaunch(int clusters, int size, int threads, size_t smem, cudaStream_t stream) {
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters) * size);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = static_cast<unsigned>(size);
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+  }
+};
+
+// Clusters of `size` CTAs that can run at once, per kernel and device.  (One
+// sixteenth off: the query has been seen to count clusters that the hardware
+// then placed one after another.)
+int clusters_at_once(const void* kernel, int size, int threads, size_t smem) {
+  struct Entry {
+    const void* kernel;
+    int dev, size, n;
+  };
+  static std::mutex mu;
+  static Entry entries[64];
+  static int used = 0;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> g(mu);
+  for (int i = 0; i < used; ++i)
+    if (entries[i].kernel == kernel && entries[i].dev == dev && entries[i].size == size) return entries[i].n;
+  int n = 0;
+  if (set_max_dynamic_smem(kernel, smem) == cudaSuccess) {
+    ClusterLaunch l(1, size, threads, smem, nullptr);
+    l.cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &l.cfg) != cudaSuccess) n = 0;
+    n -= (n + 15) / 16;
+  }
+  (void)cudaGetLastError();
+  if (used < 64) entries[used++] = Entry{kernel, dev, size, n};
+  return n;
+}
+
+// CTAs per unit on the cluster kernel, or 0: the axis of tiles.  A cluster's time
+// follows its unit's longest share, bounded by the window or the table's
+// capacity; the axis' follows the average, plus about 4 us of joining CTAs, in
+// which an SM streams some 180 KB.  Measured (axis, cluster): 1 sequence of 517,
+// 8 KV heads of 256: 12.2, 9.7 us; 8 sequences of 8, window 1024: 22.5, 20.2 us.
+template <class C>
+int cluster_size(const PagedParams& p, bool forced) {
+  const int64_t units = static_cast<int64_t>(p.B) * p.units;
+  const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
+  const int64_t keys = p.window > 0 && p.window + C::KT < cap ? p.window + C::KT : cap;
+  const double longest = static_cast<double>(keys) * C::D * 4;  // bytes of a unit
+  const void* k = reinterpret_cast<const void*>(paged_decode_mma_kernel<C>);
+  for (int c = kMaxCluster; c > 1; c /= 2) {
+    if (!forced && longest * (1.0 / c - static_cast<double>(units) / num_sms()) > 180e3) continue;
+    if (units <= clusters_at_once(k, c, C::kThreads, C::kSmem)) return c;
+  }
+  return 0;
+}
+
 template <class C>
 cudaError_t launch_mma_cfg(PagedParams p, cudaStream_t s) {
   auto k = paged_decode_mma_kernel<C>;
@@ -1145,18 +1286,30 @@ cudaError_t launch_mma_cfg(PagedParams p, cudaStream_t s) {
       return cudaErrorInvalidValue;
   }
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), C::kSmem); e != cudaSuccess) return e;
-  PdlLaunch l(dim3(p.slices), C::kThreads, C::kSmem, s);
-  cudaError_t e = cudaLaunchKernelEx(&l.cfg, k, kmap, vmap, p);
+  cudaError_t e;
+  if constexpr (C::CLUSTER) {
+    ClusterLaunch l(p.B * p.units, p.cluster, C::kThreads, C::kSmem, s);
+    e = cudaLaunchKernelEx(&l.cfg, k, kmap, vmap, p);
+  } else {
+    PdlLaunch l(dim3(p.slices), C::kThreads, C::kSmem, s);
+    e = cudaLaunchKernelEx(&l.cfg, k, kmap, vmap, p);
+  }
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 
+// p.cluster: 0 where the merge kernel has to follow
 template <int D, int NT, int KT, int SLOTS, int WARPS>
-cudaError_t launch_mma(const PagedParams& p, cudaStream_t s) {
+cudaError_t launch_mma(PagedParams& p, int variant, cudaStream_t s) {
   // A request is a box of 16 rows at least: pages of other sizes take cp.async.
   // (The strides of a tensor map end at 2^40 bytes.)
   const bool tma = p.page_size % 16 == 0 && static_cast<int64_t>(p.page_size) * D * 2 < (int64_t(1) << 40);
-  return tma ? launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, true>>(p, s)
-             : launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, false>>(p, s);
+  if (variant == kDecodeCluster && !tma) return cudaErrorNotSupported;
+  if (!tma) return launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, false>>(p, s);
+  if (variant != kDecodeStreamK)
+    p.cluster = cluster_size<MmaCfg<D, NT, KT, SLOTS, WARPS, true, true>>(p, variant == kDecodeCluster);
+  if (variant == kDecodeCluster && !p.cluster) return cudaErrorNotSupported;
+  return p.cluster ? launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, true, true>>(p, s)
+                   : launch_mma_cfg<MmaCfg<D, NT, KT, SLOTS, WARPS, true>>(p, s);
 }
 
 template <typename T, int DPL, int KT>
@@ -1227,15 +1380,21 @@ cudaError_t launch_paged_decode(const PagedDecodeArgs& a, const char** name) {
   if (use_mma(a.D, a.dtype)) {
     *name = "paged_decode_mma";
     const bool two = pl.rows == 16;
-    if (a.D == 64) e = two ? launch_mma<64, 2, 32, 8, 6>(p, a.stream) : launch_mma<64, 1, 32, 8, 6>(p, a.stream);
-    else if (a.D == 128) e = two ? launch_mma<128, 2, 32, 4, 6>(p, a.stream) : launch_mma<128, 1, 32, 4, 6>(p, a.stream);
-    else if (a.D == 256) e = two ? launch_mma<256, 2, 16, 6, 4>(p, a.stream) : launch_mma<256, 1, 16, 6, 4>(p, a.stream);
-    else e = launch_mma<512, 1, 16, 2, 6>(p, a.stream);
+    if (a.D == 64) e = two ? launch_mma<64, 2, 32, 8, 6>(p, a.variant, a.stream) : launch_mma<64, 1, 32, 8, 6>(p, a.variant, a.stream);
+    else if (a.D == 128) e = two ? launch_mma<128, 2, 32, 4, 6>(p, a.variant, a.stream) : launch_mma<128, 1, 32, 4, 6>(p, a.variant, a.stream);
+    else if (a.D == 256) e = two ? launch_mma<256, 2, 16, 6, 4>(p, a.variant, a.stream) : launch_mma<256, 1, 16, 6, 4>(p, a.variant, a.stream);
+    else e = launch_mma<512, 1, 16, 2, 6>(p, a.variant, a.stream);
   } else {
+    if (a.variant == kDecodeCluster) return cudaErrorNotSupported;
     *name = a.dtype == EXTKV_F32 ? "paged_decode_simt_f32" : "paged_decode_simt_bf16";
     e = a.dtype == EXTKV_F32 ? launch_simt_d<float>(p, a.stream) : launch_simt_d<__nv_bfloat16>(p, a.stream);
   }
   if (e != cudaSuccess) return e;
+  if (p.cluster) {
+    *name = "paged_decode_cluster";
+    note_launches(1);
+    return cudaSuccess;
+  }
   e = a.dtype == EXTKV_F32 ? launch_merge<float>(p, a.stream) : launch_merge<__nv_bfloat16>(p, a.stream);
   if (e == cudaSuccess) note_launches(2);
   return e;

@@ -405,7 +405,12 @@ int paged_kv_append(void *k_pages, void *v_pages, const void *k_new, const void 
  *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
  *     max_pages * page_size < 2^31.
  *   - bf16 with D in {64,128,256,512} runs on tensor cores, every other shape
- *     on fp32 SIMT; both split the batch's keys evenly over the GPU.
+ *     on fp32 SIMT; both split the batch's keys evenly over the GPU.  Few short
+ *     units (a small batch or a window, page_size a multiple of 16) run on a
+ *     kernel with a cluster of CTAs per (sequence, KV head, head group) instead;
+ *     EXTKV_ALGO_DECODE_STREAMK and EXTKV_ALGO_DECODE_CLUSTER force the one or
+ *     the other (EXTKV_ERR_UNSUPPORTED where the cluster kernel cannot run), and
+ *     every other extkv_set_algo setting leaves the choice to the call.
  * workspace: attention_paged_decode_workspace_size(...) bytes, 256-byte
  * aligned, as for attention_ext_kv (calls that can overlap need their own).
  */

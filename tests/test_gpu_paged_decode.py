@@ -105,21 +105,34 @@ CASES = [
 ]
 
 
+@pytest.mark.parametrize("algo", [ek.ALGO_AUTO, ek.ALGO_DECODE_STREAMK, ek.ALGO_DECODE_CLUSTER], ids=["auto", "axis", "cluster"])
 @pytest.mark.parametrize("case", CASES, ids=lambda c: f"B{len(c[0])}max{max(c[0])}_h{c[1]}-{c[2]}_d{c[3]}_p{c[4]}_w{c[5]}_{str(c[6])[6:]}")
-def test_paged_decode_matches_the_definition(case):
+def test_paged_decode_matches_the_definition(case, algo):
     lens, Hq, Hkv, D, page, window, dtype = case
     scale = 1.0 / math.sqrt(D)
+    mma = dtype == torch.bfloat16 and D in (64, 128, 256, 512)
     q, k, v, table, nonpad = make(lens, Hq, Hkv, D, page, dtype, window=window)
-    y = run(q, k, v, table, nonpad, scale, window)
+    units = len(lens) * Hkv * -(-(Hq // Hkv) // (16 if Hq // Hkv > 8 and D <= 256 else 8))
+    with ek.use_algo(algo):
+        if algo == ek.ALGO_DECODE_CLUSTER and (not mma or page % 16 or units > 80):
+            with pytest.raises(ek.ExtKVError) as e:
+                run(q, k, v, table, nonpad, scale, window)
+            assert e.value.code == ek.EXTKV_ERR_UNSUPPORTED
+            return
+        y = run(q, k, v, table, nonpad, scale, window)
+        name = ek.extkv_last_kernel()
+        # the same bits again, whatever the timing
+        assert torch.equal(y, run(q, k, v, table, nonpad, scale, window))
     ref, tol = reference(q, k, v, table, lens, window, scale)
     check(y, ref, tol, "y")
     for b, n in enumerate(lens):
         if n == 0:
             assert torch.count_nonzero(y[b]) == 0
-    # the same bits again, whatever the timing
-    assert torch.equal(y, run(q, k, v, table, nonpad, scale, window))
-    mma = dtype == torch.bfloat16 and D in (64, 128, 256, 512)
-    assert ek.extkv_last_kernel() == ("paged_decode_mma" if mma else f"paged_decode_simt_{'f32' if dtype == torch.float32 else 'bf16'}")
+    if not mma:
+        assert name == f"paged_decode_simt_{'f32' if dtype == torch.float32 else 'bf16'}"
+    else:
+        assert name in {ek.ALGO_AUTO: ("paged_decode_mma", "paged_decode_cluster"), ek.ALGO_DECODE_STREAMK: ("paged_decode_mma",),
+                        ek.ALGO_DECODE_CLUSTER: ("paged_decode_cluster",)}[algo]
 
 
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
@@ -134,7 +147,7 @@ def test_q_rows_may_be_strided(dtype):
 
 
 @pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float32, 64)])
-def test_extreme_scores(dtype, D):
+def test_extreme_scores(dtype, D, each_kernel):
     """A peaked softmax (scores of hundreds), equal keys, and a key far above the rest."""
     lens = (400, 77)
     q, k, v, table, nonpad = make(lens, 4, 2, D, 16, dtype, sigma=40.0)
@@ -147,8 +160,14 @@ def test_extreme_scores(dtype, D):
     check(y, ref, tol, "equal")
 
 
+@pytest.fixture(params=[ek.ALGO_DECODE_STREAMK, ek.ALGO_AUTO], ids=["axis", "auto"])
+def each_kernel(request):
+    with ek.use_algo(request.param):
+        yield
+
+
 @pytest.mark.parametrize("dtype,D", [(torch.bfloat16, 128), (torch.float32, 64), (torch.bfloat16, 512)])
-def test_bad_lengths_and_pages_are_flagged_and_skipped(dtype, D):
+def test_bad_lengths_and_pages_are_flagged_and_skipped(dtype, D, each_kernel):
     lens = (100, 40, 64, 200)
     q, k, v, table, nonpad = make(lens, 4, 2, D, 16, dtype)
     scale = 0.125
@@ -187,7 +206,7 @@ def test_bad_lengths_and_pages_are_flagged_and_skipped(dtype, D):
     assert torch.count_nonzero(y[2]) == 0 and torch.isfinite(y.float()).all()
 
 
-def test_the_length_limits():
+def test_the_length_limits(each_kernel):
     """Full tables: every slot of every page live, lengths at the capacity."""
     for D, page, dtype in ((128, 16, torch.bfloat16), (256, 5, torch.bfloat16), (64, 16, torch.float32)):
         lens = (page * 9, page * 9)
@@ -198,7 +217,7 @@ def test_the_length_limits():
         check(y, ref, tol, "full")
 
 
-def test_an_empty_table_and_an_empty_batch():
+def test_an_empty_table_and_an_empty_batch(each_kernel):
     q, k, v, table, nonpad = make((0, 0), 4, 2, 128, 16, torch.bfloat16)
     empty = table[:, :0].contiguous()
     y = run(q, k, v, empty, nonpad, 1.0, 0)
@@ -206,7 +225,7 @@ def test_an_empty_table_and_an_empty_batch():
     ek.attention_paged_decode(q[:0], q[:0], k, v, table[:0], nonpad[:0], 1.0)
 
 
-def test_sequences_may_share_pages():
+def test_sequences_may_share_pages(each_kernel):
     """Two sequences with one prompt's pages in common."""
     lens = (200, 200)
     q, k, v, table, nonpad = make(lens, 8, 2, 128, 16, torch.bfloat16)
@@ -237,7 +256,7 @@ def test_offsets_past_32_bits():
     check(y, ref, tol, "far pages")
 
 
-def test_other_stream_prepared_and_captured():
+def test_other_stream_prepared_and_captured(each_kernel):
     lens = (300, 1, 0, 2000)
     q, k, v, table, nonpad = make(lens, 8, 4, 128, 16, torch.bfloat16)
     good = run(q, k, v, table, nonpad, 0.1, 0)
@@ -304,7 +323,7 @@ def test_one_sequence_over_every_warp(D, keys, per_warp):
     assert float((y.double() - ref).norm() / ref.norm()) < 2.0 ** -7
 
 
-def test_a_wait_that_runs_out_is_reported():
+def test_a_wait_that_runs_out_is_reported(each_kernel):
     """A poll limit of zero: the ring's waits give up, the status word says so, and
     the next call is whole again."""
     lens = (300, 77, 0, 5000)
@@ -320,7 +339,7 @@ def test_a_wait_that_runs_out_is_reported():
 
 
 @pytest.mark.parametrize("D,g,page", [(64, 4, 16), (128, 2, 64), (128, 16, 16), (256, 2, 32), (512, 8, 16), (128, 3, 7), (96, 2, 16)])
-def test_the_same_bits_from_cold_and_warm_caches(D, g, page):
+def test_the_same_bits_from_cold_and_warm_caches(D, g, page, each_kernel):
     """Copies that land late, early and in other orders change no bit."""
     lens = (4000, 17, 900, 0, 2500, 333)
     q, k, v, table, nonpad = make(lens, 2 * g, 2, D, page, torch.bfloat16)
