@@ -33,6 +33,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxRows = 16;  // rows per CTA
 constexpr int kUnroll = 2;   // vectors in flight per thread
 constexpr int kMinCtas = 5;
+constexpr int kMaxHeadsPerCta = 4096;
 
 struct Tensor {
   const void* src;
@@ -127,7 +128,9 @@ __device__ __forceinline__ void pack(Vec<T, VW>& x, const float (&f)[VW]) {
   }
 }
 
-// x / d for x and d below 2^16.
+// x / d, exact while x * d < 2^32: a CTA divides (row, head) numbers, below
+// kMaxRows * kMaxHeadsPerCta, by its heads.
+static_assert(int64_t(kMaxRows) * kMaxHeadsPerCta * kMaxHeadsPerCta <= (int64_t(1) << 32), "SmallDiv");
 struct SmallDiv {
   uint32_t d, inv;
   __device__ __forceinline__ explicit SmallDiv(int d_) : d(d_), inv(d_ > 1 ? 0xffffffffu / d_ + 1 : 0) {}
@@ -387,7 +390,7 @@ cudaError_t launch_rotary(const RotaryArgs& a) {
   // angles again); many rows: as many rows a CTA as make one wave of CTAs.
   const int heads = a.q.heads + a.k.heads + a.v.heads;
   const int64_t ctas = int64_t(num_sms()) * kMinCtas;
-  int hpc = heads;
+  int hpc = std::min(heads, kMaxHeadsPerCta);
   while (hpc > 4 && p.n_rows * ((heads + hpc - 1) / hpc) < ctas) hpc = (hpc + 1) / 2;
   const int64_t rpc = hpc == heads ? std::min<int64_t>(kMaxRows, (p.n_rows + ctas - 1) / ctas) : 1;
   const int64_t gx = (p.n_rows + rpc - 1) / rpc;

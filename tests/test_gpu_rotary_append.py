@@ -248,3 +248,19 @@ def test_append_captured_and_on_another_stream():
     ek.paged_kv_append(want_k, want_v, k, v, table, widx, rotary=spec, q_out=want_q, q=q)
     torch.cuda.synchronize()
     assert torch.equal(got_k, want_k) and torch.equal(got_v, want_v) and torch.equal(got_q, want_q)
+
+
+def test_thousands_of_heads():
+    """More heads than one CTA numbers: every row and head still lands once."""
+    T, H, D = 800, 65535, 8
+    gen = torch.Generator(device="cuda").manual_seed(8)
+    k, v = (torch.randint(-30000, 30000, (T, H, D), dtype=torch.int16, device="cuda", generator=gen).view(torch.bfloat16)
+            for _ in range(2))
+    kp, vp = (torch.zeros((T, H, 1, D), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = torch.arange(T, device="cuda")[None].contiguous()
+    cu = torch.tensor([0, T], dtype=torch.int64, device="cuda")
+    st = ek.new_status()
+    ek.paged_kv_append(kp, vp, k, v, table, torch.zeros(1, dtype=torch.int64, device="cuda"), cu_seqlens=cu, status=st)
+    assert ek.extkv_read_status(st) == ek.EXTKV_OK
+    assert torch.equal(kp[:, :, 0].view(torch.int16), k.view(torch.int16))
+    assert torch.equal(vp[:, :, 0].view(torch.int16), v.view(torch.int16))
