@@ -225,7 +225,7 @@ template <int KT>
 struct TileRows {
   int64_t page;
   int off, u;
-  bool live;
+  bool live, lead;  // lead: the page's first live row of this tile
   __device__ __forceinline__ void look_up(const PagedParams& p, const Cursor<KT>& c) {
     const int lane = threadIdx.x & 31;
     const int j = c.key0() + lane;
@@ -233,9 +233,11 @@ struct TileRows {
     u = c.u;
     off = 0;
     page = -1;
+    lead = false;
     if (live) {
       const int pg = j / p.page_size;
       off = j - pg * p.page_size;
+      lead = lane == 0 || off == 0 || j == c.keys.lo;
       page = p.table[static_cast<int64_t>(c.b) * p.max_pages + pg];
     }
   }
@@ -243,7 +245,7 @@ struct TileRows {
   __device__ __forceinline__ uint32_t row(const PagedParams& p) const {
     if (!live) return ~0u;
     if (page < 0 || page >= p.num_pages) {
-      if (u == 0 && ((threadIdx.x & 31) == 0 || off == 0)) report(p.status, EXTKV_DEV_BAD_PAGE);
+      if (u == 0 && lead) report(p.status, EXTKV_DEV_BAD_PAGE);
       return ~0u;
     }
     const int64_t r = (page * p.Hkv + u / p.groups) * p.page_size + off;

@@ -206,6 +206,50 @@ def test_bad_lengths_and_pages_are_flagged_and_skipped(dtype, D, each_kernel):
     assert torch.count_nonzero(y[2]) == 0 and torch.isfinite(y.float()).all()
 
 
+@pytest.mark.parametrize("dtype,D,page", [(torch.bfloat16, 128, 7), (torch.float32, 64, 7), (torch.bfloat16, 128, 16)])
+def test_a_bad_page_that_a_window_enters_midway_is_flagged(dtype, D, page, each_kernel):
+    """The window's first key is neither a page's nor a tile's first row."""
+    n, window = 100, 47
+    q, k, v, table, nonpad = make((n,), 4, 2, D, page, dtype)
+    lo = n - window
+    assert lo % page and lo % 16
+    table[0, lo // page] = -1
+    y = torch.empty((1, 4, D), dtype=dtype, device="cuda")
+    st = ek.new_status()
+    ek.attention_paged_decode(y, q, k, v, table, nonpad, 0.1, window=window, status=st)
+    assert ek.extkv_read_status(st) == ek.EXTKV_ERR_DEVICE and int(st[0]) == ek.EXTKV_DEV_BAD_PAGE
+    good = make((n,), 4, 2, D, page, dtype)[3]
+    j = torch.arange((lo // page + 1) * page, n, device="cuda")
+    at, off = good[0][j // page], j % page
+    ok = torch.ones((2, len(j)), dtype=torch.bool, device="cuda")
+    p_bf16 = dtype == torch.bfloat16
+    for h in range(2):
+        o, pv, size = attention_rows(q[0, 2 * h:2 * h + 2], k[at, h, off], v[at, h, off], ok, 0.1)
+        check(y[0, 2 * h:2 * h + 2], o, bound(o, pv, size, D, n, dtype, p_bf16), "rest")
+
+
+def test_two_streams_at_once(each_kernel):
+    """Calls with workspaces of their own, of both forms, side by side on two streams."""
+    sets = []
+    for i, (lens, Hq, Hkv, D) in enumerate((((517,), 16, 8, 256), ((4000, 300, 1, 77), 8, 2, 128))):
+        q, k, v, table, nonpad = make(lens, Hq, Hkv, D, 16, torch.bfloat16, seed=i)
+        good = run(q, k, v, table, nonpad, 0.1, 0)
+        s = torch.cuda.Stream()
+        y = torch.zeros_like(good)
+        sets.append((y, good, ek.prepare_attention_paged_decode(y, q, k, v, table, nonpad, 0.1, stream=s)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for y, _, _ in sets:
+            y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            for _, _, call in sets:
+                call()
+        torch.cuda.synchronize()
+        for y, good, _ in sets:
+            assert torch.equal(y, good)
+
+
 def test_the_length_limits(each_kernel):
     """Full tables: every slot of every page live, lengths at the capacity."""
     for D, page, dtype in ((128, 16, torch.bfloat16), (256, 5, torch.bfloat16), (64, 16, torch.float32)):
