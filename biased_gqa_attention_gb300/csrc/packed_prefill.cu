@@ -29,7 +29,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   ptx::grid_launch_dependents();
   __syncthreads();
   bool mine_bad = false;
-  for (int b = tid; b <= p.B; b += kPlanThreads) {
+  for (int64_t b = tid; b <= p.B; b += kPlanThreads) {
     const int64_t x = p.cu[b];
     mine_bad |= x < 0 || x > p.T || (b > 0 && p.cu[b - 1] > x);
   }

@@ -433,7 +433,7 @@ size_t attention_paged_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv,
  *     of v that holds an infinity or a NaN may reach every row of its own
  *     sequence, as 0 * infinity does.
  *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
- *     T < 2^31 - 256.
+ *     T + B <= 2^31 - 256.
  *   - bf16 with D in {64,128,256} runs on the tcgen05 tensor cores, every other
  *     shape on fp32 SIMT.  P is rounded to bf16 for the P.V product there (its
  *     sum is taken before that).

@@ -242,3 +242,41 @@ def test_the_same_bits_from_cold_and_warm_caches(D, window):
         if i % 3 == 2:
             k.sum()  # K warm, V cold
         assert torch.equal(run(q, k, v, cu, 1.0 / math.sqrt(D), True, window), good), i
+
+
+def test_two_streams_at_once():
+    """Calls with workspaces of their own, side by side on two streams."""
+    sets = []
+    for lens, Hq, Hkv, D in (((700, 1, 200), 16, 8, 256), ((900, 64), 8, 4, 128), ((500, 500), 4, 2, 64)):
+        q, k, v, cu = make(lens, Hq, Hkv, D, torch.bfloat16)
+        good = run(q, k, v, cu, 0.1, True, 0)
+        s = torch.cuda.Stream()
+        y = torch.zeros_like(good)
+        sets.append((y, good, ek.prepare_attention_packed_prefill(y, q, k, v, cu, 0.1, stream=s)))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for y, _, _ in sets:
+            y.zero_()
+        torch.cuda.synchronize()
+        for _ in range(10):
+            for _, _, call in sets:
+                call()
+        torch.cuda.synchronize()
+        for y, good, _ in sets:
+            assert torch.equal(y, good)
+
+
+def test_a_recorded_step():
+    q, k, v, cu = make((100, 1, 300), 8, 2, 128, torch.bfloat16)
+    good = run(q, k, v, cu, 0.1, True, 0)
+    y = torch.zeros_like(good)
+    ws = torch.empty(ek.attention_packed_prefill_workspace_size(q.shape[0], 3, 8, 2, 128, torch.bfloat16), dtype=torch.uint8,
+                     device="cuda")
+    with ek.StepRecorder() as rec:
+        ek.attention_packed_prefill(y, q, k, v, cu, 0.1, workspace=ws, stream=rec.stream)
+    for _ in range(2):
+        y.zero_()
+        torch.cuda.synchronize()
+        rec.step()
+        torch.cuda.synchronize()
+        assert torch.equal(y, good)
