@@ -83,7 +83,9 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 // ---- SIMT (fp32, other head sizes) ---------------------------------------------------
 // A CTA takes a tile of 32 query rows (tokens by heads of one KV head), eight a
 // warp, and streams the keys through two shared-memory stages that its four
-// warps share.
+// warps share.  Bound by the fp32 lanes for long prompts, by the chain of key
+// tiles of one CTA for short ones: 218 rows in four prompts, 4 heads of 64, fp32:
+// 20 us (23 with the rows' softmax steps one after another and q staged row by row).
 
 constexpr int kWarps = 4;
 constexpr int kTileRows = kWarps * kRows;

@@ -143,67 +143,67 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   if (warp < 8) {
     reg_dec<72>();
     if (warp == 0) {
-    // ---------------- loads ----------------
-    int u = 0, nq[2] = {0, 0}, tails = 0;
-    bool ok = true;
-    auto acquire = [&]() -> bool {  // the next unit of the ring is free
-      return u < C::kUnits || wait_or_abort(&bar.u_empty[u % C::kUnits], ((u / C::kUnits) - 1) & 1, abort, lim);
-    };
-    auto load_q = [&](const Work& w, int t) -> bool {
-      if (w.lo[t] >= w.hi[t]) return true;
-      if (nq[t] && !wait_or_abort(&bar.q_empty[t], (nq[t] - 1) & 1, abort, lim)) return false;
-      ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kQTile);
-      ptx::tma_load_4d(sm + t * C::kQTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
-      ++nq[t];
-      return true;
-    };
-    Rounds rounds(n_work, blockIdx.x, gridDim.x);
-    for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at<KN>(p, wi);
-      if (lane == 0) ok = load_q(w, 0);
-      for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
-        const int key0 = w.row0 + kt * KN;
-        const bool tail = (kt + 1) * KN > w.len;  // keys of the next sequence behind the last one
-        if (lane == 0) {
-          ok = ok && acquire();
-          if (ok) {
-            uint64_t* full = &bar.u_full[u % C::kUnits];
-            ptx::mbar_arrive_expect_tx(full, C::kTile);
-            ptx::tma_load_4d(sKV + (u % C::kUnits) * C::kTile, &kmap, full, 0, key0, w.hk, 0);
+      // ---------------- loads ----------------
+      int u = 0, nq[2] = {0, 0}, tails = 0;
+      bool ok = true;
+      auto acquire = [&]() -> bool {  // the next unit of the ring is free
+        return u < C::kUnits || wait_or_abort(&bar.u_empty[u % C::kUnits], ((u / C::kUnits) - 1) & 1, abort, lim);
+      };
+      auto load_q = [&](const Work& w, int t) -> bool {
+        if (w.lo[t] >= w.hi[t]) return true;
+        if (nq[t] && !wait_or_abort(&bar.q_empty[t], (nq[t] - 1) & 1, abort, lim)) return false;
+        ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kQTile);
+        ptx::tma_load_4d(sm + t * C::kQTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
+        ++nq[t];
+        return true;
+      };
+      Rounds rounds(n_work, blockIdx.x, gridDim.x);
+      for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
+        const Work w = work_at<KN>(p, wi);
+        if (lane == 0) ok = load_q(w, 0);
+        for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
+          const int key0 = w.row0 + kt * KN;
+          const bool tail = (kt + 1) * KN > w.len;  // keys of the next sequence behind the last one
+          if (lane == 0) {
+            ok = ok && acquire();
+            if (ok) {
+              uint64_t* full = &bar.u_full[u % C::kUnits];
+              ptx::mbar_arrive_expect_tx(full, C::kTile);
+              ptx::tma_load_4d(sKV + (u % C::kUnits) * C::kTile, &kmap, full, 0, key0, w.hk, 0);
+            }
+            if (ok && kt == w.k_lo) ok = load_q(w, 1);
           }
-          if (ok && kt == w.k_lo) ok = load_q(w, 1);
-        }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        ++u;
-        uint8_t* dst = sKV + (u % C::kUnits) * C::kTile;
-        if (lane == 0) {
-          ok = acquire();
-          if (ok) {
-            uint64_t* full = tail ? &bar.v_tail : &bar.u_full[u % C::kUnits];
-            ptx::mbar_arrive_expect_tx(full, C::kTile);
-            ptx::tma_load_4d(dst, &vmap, full, 0, key0, w.hk, 0);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          ++u;
+          uint8_t* dst = sKV + (u % C::kUnits) * C::kTile;
+          if (lane == 0) {
+            ok = acquire();
+            if (ok) {
+              uint64_t* full = tail ? &bar.v_tail : &bar.u_full[u % C::kUnits];
+              ptx::mbar_arrive_expect_tx(full, C::kTile);
+              ptx::tma_load_4d(dst, &vmap, full, 0, key0, w.hk, 0);
+            }
           }
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          if (tail) {
+            if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_tail, tails & 1, abort, lim)))) break;
+            ++tails;
+            zero_rows<D>(dst, w.len - kt * KN, KN, lane);
+            if (lane == 0) ptx::mbar_arrive(&bar.u_full[u % C::kUnits]);
+          }
+          ++u;
         }
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
-        if (tail) {
-          if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.v_tail, tails & 1, abort, lim)))) break;
-          ++tails;
-          zero_rows<D>(dst, w.len - kt * KN, KN, lane);
-          if (lane == 0) ptx::mbar_arrive(&bar.u_full[u % C::kUnits]);
-        }
-        ++u;
       }
-    }
-    if (lane == 0 && *abort) {  // copies still in flight land before the CTA leaves
-      for (int x = u >= C::kUnits ? u - C::kUnits + 1 : 0; x <= u; ++x)
-        ptx::mbar_wait_bounded(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, kWaitPolls >> 6);
-      for (int t = 0; t < 2; ++t)
-        if (nq[t]) ptx::mbar_wait_bounded(&bar.q_full[t], (nq[t] - 1) & 1, kWaitPolls >> 6);
-      ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
-    }
-    __syncwarp();
+      if (lane == 0 && *abort) {  // copies still in flight land before the CTA leaves
+        for (int x = u >= C::kUnits ? u - C::kUnits + 1 : 0; x <= u; ++x)
+          ptx::mbar_wait_bounded(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, kWaitPolls >> 6);
+        for (int t = 0; t < 2; ++t)
+          if (nq[t]) ptx::mbar_wait_bounded(&bar.q_full[t], (nq[t] - 1) & 1, kWaitPolls >> 6);
+        ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
+      }
+      __syncwarp();
     } else if (warp < 3) {
       // ---------------- Q K^T of one query tile ----------------
       if (lane == 0) {
