@@ -9,9 +9,10 @@
 namespace extkv {
 
 // One tile of queries: tokens tok0 .. of the sequence whose first row is
-// `row0` and which has `len` tokens.
+// `row0` and which has `len` tokens; tile_tok of them, or half as many where the
+// item is split over its keys (tensor-core kernel for head sizes 64 and 128).
 struct PackedItem {
-  int row0, len, tok0, pad;
+  int row0, len, tok0, split;
 };
 
 struct PackedParams {
@@ -25,6 +26,7 @@ struct PackedParams {
   int64_t q_stride, k_stride, v_stride;
   int pk;        // query heads of one KV head in a tile (a power of two that divides g)
   int tile_tok;  // tokens of a tile
+  int ctas;      // CTAs that share the list where items may be split, or 0
   int heads;     // head groups: Hq / pk
   int max_items;
   int* count;         // items, written by the plan kernel
@@ -33,9 +35,9 @@ struct PackedParams {
   uint32_t wait_limit;
 };
 
-// The keys some row of the tile attends, [lo, hi).
-__device__ __forceinline__ int2 item_keys(const PackedParams& p, int len, int tok0) {
-  const int last = min(len, tok0 + p.tile_tok);
+// The keys some of `tokens` rows from tok0 on attends, [lo, hi).
+__device__ __forceinline__ int2 item_keys(const PackedParams& p, int len, int tok0, int tokens) {
+  const int last = min(len, tok0 + tokens);
   return make_int2(p.window > 0 ? max(0, tok0 - p.window + 1) : 0, p.causal ? last : len);
 }
 

@@ -13,18 +13,39 @@ namespace extkv {
 
 namespace {
 
+constexpr int kSplitAt = 3;     // halves of a CTA's share of all work
+constexpr int kSplitLeast = 2;  // in tiles of 128 keys
+
+// in tiles of 128 keys
+__device__ __forceinline__ int item_cost(const PackedParams& p, int len, int tok0, int tokens) {
+  const int2 k = item_keys(p, len, tok0, tokens);
+  return (k.y + 127) / 128 - k.x / 128;
+}
+
 // One CTA.  A causal prompt's tiles cost from one to len / 128 key tiles, so the
 // list is sorted by cost, dearest first (a counting sort over 1024 cost
 // classes): CTAs that take items in turn then end together.  The order within a
 // class follows the atomics; every item is computed alone, so no result
 // depends on it.  Also checks cu_seqlens: a bad one leaves an empty list.
+//
+// In a small batch (p.ctas) an item that costs more than kSplitAt / 2 times a CTA's
+// share of all work is listed as two of half its tokens, whose keys are split over
+// the CTA's two query tiles: they take half as long one after another.  Otherwise a
+// short batch waits for its longest prompt's last items.  Measured without and with:
+// one prompt of 2047 rows, 8 heads of 128, 41 and 33 us; four of 50 to 3000, 8 heads
+// of 64, 55 and 42; twelve of 1 to 2047, 8 heads of 128, 38.2 and 36.4; four of 900,
+// 27 and 25 (splitting from one share on: 31).
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedParams p) {
   __shared__ int hist[1024];
   __shared__ int warp_sum[32];
   __shared__ int bad;
+  __shared__ unsigned long long total_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   hist[tid] = 0;
-  if (tid == 0) bad = 0;
+  if (tid == 0) {
+    bad = 0;
+    total_s = 0;
+  }
   ptx::grid_dependency_wait();
   ptx::grid_launch_dependents();
   __syncthreads();
@@ -42,40 +63,58 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     }
     return;
   }
-  const int most = p.T / 128 + 2;  // an item's cost is below this
-  auto cls = [&](int len, int tok0) {
-    const int2 k = item_keys(p, len, tok0);
-    const int cost = (k.y + 127) / 128 - k.x / 128;
-    return 1023 - static_cast<int>(static_cast<int64_t>(cost) * 1023 / most);
-  };
-  // a warp per sequence, a lane per tile
-  for (int b = warp; b < p.B; b += kPlanThreads / 32) {
-    const int len = static_cast<int>(p.cu[b + 1] - p.cu[b]);
-    for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok)
-      atomicAdd(&hist[cls(len, static_cast<int>(t))], 1);
-  }
-  __syncthreads();
-  const int n = hist[tid];
-  int inc = n;
+  const float to_class = 1023.f / static_cast<float>(p.T / 128 + 2);  // an item's cost is below that
+  int64_t limit = INT_MAX;  // items that cost more are split
+  // Passes over all tiles: the total cost, the classes' sizes, the items.  One loop
+  // (not unrolled), since the kernel's time is mostly fetching its code.
+#pragma unroll 1
+  for (int pass = p.ctas ? 0 : 1; pass < 3; ++pass) {
+    int64_t sum = 0;
+    // a warp per sequence, a lane per tile
+#pragma unroll 1
+    for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+      const int row0 = static_cast<int>(p.cu[b]), len = static_cast<int>(p.cu[b + 1]) - row0;
+#pragma unroll 1
+      for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok) {
+        int tok = static_cast<int>(t), tokens = p.tile_tok;
+        int cost = item_cost(p, len, tok, tokens);
+        if (pass == 0) {
+          sum += cost;
+          continue;
+        }
+        const int split = cost > limit;
+        if (split) tokens /= 2;
+#pragma unroll 1
+        for (int end = min(len, tok + p.tile_tok); tok < end; tok += tokens) {
+          if (split) cost = (item_cost(p, len, tok, tokens) + 1) / 2;
+          const int at = atomicAdd(&hist[1023 - min(1023, static_cast<int>(cost * to_class))], 1);
+          if (pass == 2 && at < p.max_items && EXTKV_IN(at, 1, p.max_items, p.status))
+            p.items[at] = PackedItem{row0, len, tok, split};
+        }
+      }
+    }
+    if (pass == 0) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) warp_sum[warp] = inc;
-  __syncthreads();
-  int off = 0;
-  for (int w = 0; w < warp; ++w) off += warp_sum[w];
-  __syncthreads();
-  hist[tid] = off + inc - n;
-  if (tid == kPlanThreads - 1) *p.count = min(off + inc, p.max_items);
-  __syncthreads();
-  for (int b = warp; b < p.B; b += kPlanThreads / 32) {
-    const int row0 = static_cast<int>(p.cu[b]), len = static_cast<int>(p.cu[b + 1]) - row0;
-    for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok) {
-      const int at = atomicAdd(&hist[cls(len, static_cast<int>(t))], 1);
-      if (at < p.max_items && EXTKV_IN(at, 1, p.max_items, p.status))
-        p.items[at] = PackedItem{row0, len, static_cast<int>(t), 0};
+      for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+      if (lane == 0 && sum) atomicAdd(&total_s, static_cast<unsigned long long>(sum));
+      __syncthreads();
+      limit = max(int64_t(kSplitLeast), static_cast<int64_t>(total_s) * p.heads * kSplitAt / (2 * p.ctas));
+    } else if (pass == 1) {  // each class's first place in the list
+      __syncthreads();
+      const int n = hist[tid];
+      int inc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      if (lane == 31) warp_sum[warp] = inc;
+      __syncthreads();
+      int off = 0;
+      for (int w = 0; w < warp; ++w) off += warp_sum[w];
+      hist[tid] = off + inc - n;
+      if (tid == kPlanThreads - 1) *p.count = min(off + inc, p.max_items);
+      __syncthreads();
     }
   }
 }
@@ -122,7 +161,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
     if (!EXTKV_IN(at, 1, p.max_items, p.status)) break;
     const PackedItem item = p.items[at];
     const int h0 = static_cast<int>(w - at * p.heads) * p.pk, hk = h0 / p.g;
-    const int2 keys = item_keys(p, item.len, item.tok0);
+    const int2 keys = item_keys(p, item.len, item.tok0, p.tile_tok);
     st.clear();
     auto load = [&](int t, int s) {
       const int k0 = keys.x + t * KT;
@@ -219,19 +258,22 @@ int pack_heads(int64_t g, int cap) {
 // Rows of a work item and the query heads packed into it.  The tensor-core
 // kernel's query tiles are M = 128 rows.
 struct Shape {
-  bool tc;
+  bool tc, split;  // split: items may be of half the rows
   int rows, pk;
 };
 
 Shape shape_of(int64_t Hq, int64_t Hkv, int64_t D, int dtype) {
   Shape s;
   s.tc = packed_tc_supported(D, dtype);
+  s.split = s.tc && D != 256;
   s.rows = s.tc ? kPackedTcRows : kTileRows;
   s.pk = pack_heads(Hq / Hkv, s.tc ? 128 : kTileRows);
   return s;
 }
 
-int64_t max_items(const Shape& s, int64_t T, int64_t B) { return T / (s.rows / s.pk) + B + 1; }
+int64_t max_items(const Shape& s, int64_t T, int64_t B) {
+  return T / (s.rows / s.pk / (s.split ? 2 : 1)) + B + 1;
+}
 
 }  // namespace
 
@@ -263,6 +305,10 @@ cudaError_t launch_packed(const PackedArgs& a, const char** name) {
   p.tile_tok = sh.rows / sh.pk;
   p.heads = p.Hq / p.pk;
   p.max_items = static_cast<int>(max_items(sh, a.T, a.B));
+  // Three tiles and more for two CTAs balance without splits, whose pass over the list
+  // then costs more than it gives (2047 rows of 32 heads, 256 tiles: 44 us without,
+  // 47 with); 256 rows and fewer have no item to split.
+  p.ctas = sh.split && 2 * (a.T / p.tile_tok) * p.heads < 3 * num_sms() && a.T > 128 * kSplitLeast ? num_sms() : 0;
   uint8_t* ws = static_cast<uint8_t*>(a.workspace);
   p.count = reinterpret_cast<int*>(ws);
   p.items = reinterpret_cast<PackedItem*>(ws + 256);

@@ -6,7 +6,10 @@
 //
 // A persistent CTA per SM takes query tiles from the plan's list (dearest
 // first, rounds taken in alternating order).  An item is 256 query rows, two
-// M = 128 tiles A and B of one KV head's (token, head) rows.
+// M = 128 tiles A and B of one KV head's (token, head) rows; or, where one item
+// would outlast a CTA's share of the batch, 128 rows: then A takes its first, third, ..
+// key tile and B the others, and A's softmax warps join the two, B's rows of O
+// straight from tensor memory.
 //   warp 0       loads: Q tiles, then K and V tiles of KN keys through a ring of
 //                shared-memory units (TMA, 128-byte swizzle)
 //   warps 1, 2   issue Q K^T of tile A and of tile B
@@ -38,17 +41,20 @@ using namespace packed;
 
 constexpr int kMaxUnits = 8;
 
+// barriers, then B's (max, sum) of each row for the join
+constexpr int kBarBytes = 512, kJoinBytes = kBM * 8;
+
 template <int D>
 struct Cfg {
   static constexpr int kThreads = 512;
   static constexpr int KN = D == 64 ? 128 : 80;  // keys of a tile
   static constexpr int kPart = D == 64 ? 64 : 48;  // keys of P released first
   static constexpr int kQTile = kBM * D * 2, kTile = KN * D * 2;  // bytes of a Q and of a K or V tile
-  static constexpr int kFit = (232448 - 2048 - 2 * kQTile) / kTile;
+  static constexpr int kFit = (232448 - 1024 - kBarBytes - kJoinBytes - 2 * kQTile) / kTile;
   static constexpr int kUnits = kFit < kMaxUnits ? kFit : kMaxUnits;
   static constexpr int kOffKV = 2 * kQTile;
   static constexpr int kOffBar = kOffKV + kUnits * kTile;
-  static constexpr int kSmem = kOffBar + 512 + 1024;
+  static constexpr int kSmem = kOffBar + kBarBytes + kJoinBytes + 1024;
   // tensor memory of a tile: S, P, O
   static constexpr uint32_t kStride = 256, kPCol = KN, kOCol = kStride - D;
   static constexpr uint32_t kTmemCols = 512;
@@ -65,11 +71,11 @@ struct Bars {
   uint64_t q_full[2], q_empty[2];
   uint64_t u_full[kMaxUnits], u_empty[kMaxUnits];
   uint64_t s_full[2], s_free[2], p_full[2][2], pv_done[2], o_full[2], o_free[2];  // p_full: of each part of P
-  uint64_t v_tail, drain[4];
+  uint64_t v_tail, drain[4], join;
   uint32_t tmem_base;
   int abort;
 };
-static_assert(sizeof(Bars) <= 512, "barrier block");
+static_assert(sizeof(Bars) <= kBarBytes, "barrier block");
 
 // Registers of the calling warpgroup; 256 * 72 + 256 * 176 <= 512 * 128.
 template <int N>
@@ -81,7 +87,9 @@ __device__ __forceinline__ void reg_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
 }
 
-template <int D>
+// SPLIT: the list may hold split items (the case above, which has none: 391 us
+// without and 398 with).
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     packed_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap, const PackedParams p) {
@@ -91,6 +99,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   uint8_t* sm = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   Bars& bar = *reinterpret_cast<Bars*>(sm + C::kOffBar);
   uint8_t* sKV = sm + C::kOffKV;
+  float2* join_ml = reinterpret_cast<float2*>(sm + C::kOffBar + kBarBytes);
   volatile int* abort = &bar.abort;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const uint32_t lim = p.wait_limit;
@@ -112,6 +121,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       ptx::mbar_init(&bar.u_empty[u], 2);
     }
     ptx::mbar_init(&bar.v_tail, 1);
+    ptx::mbar_init(&bar.join, 128);
     for (int t = 0; t < 4; ++t) ptx::mbar_init(&bar.drain[t], 1);
     bar.abort = 0;
     ptx::fence_mbar_init();
@@ -131,7 +141,6 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
   const uint32_t tbase = bar.tmem_base;
   ptx::grid_dependency_wait();  // the plan, and what the caller ran before it
   const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
-  const int tt = p.tile_tok / 2;
 
   // every MMA an issuer issued has completed before tensor memory is released
   auto drain = [&](bool issued, int who) {
@@ -153,13 +162,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         if (w.lo[t] >= w.hi[t]) return true;
         if (nq[t] && !wait_or_abort(&bar.q_empty[t], (nq[t] - 1) & 1, abort, lim)) return false;
         ptx::mbar_arrive_expect_tx(&bar.q_full[t], C::kQTile);
-        ptx::tma_load_4d(sm + t * C::kQTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + w.tok0 + t * tt, 0);
+        ptx::tma_load_4d(sm + t * C::kQTile, &qmap, &bar.q_full[t], 0, w.h0, w.row0 + (t ? w.tok[1] : w.tok[0]), 0);
         ++nq[t];
         return true;
       };
       Rounds rounds(n_work, blockIdx.x, gridDim.x);
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at<KN>(p, wi);
+        const Work w = work_at<KN, SPLIT>(p, wi);
         if (lane == 0) ok = load_q(w, 0);
         for (int kt = w.k_lo; kt < w.k_hi; ++kt) {
           const int key0 = w.row0 + kt * KN;
@@ -215,13 +224,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         bool ok = true, issued = false;
         Rounds rounds(n_work, blockIdx.x, gridDim.x);
         for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-          const Work w = work_at<KN>(p, wi);
+          const Work w = work_at<KN, SPLIT>(p, wi);
           const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
           issued = true;
           nq += lo < hi;
           for (int kt = w.k_lo; kt < w.k_hi; ++kt, u += 2) {
             if (!(ok = wait_or_abort(&bar.u_full[u % C::kUnits], (u / C::kUnits) & 1, abort, lim))) break;
-            if (kt >= lo && kt < hi) {
+            if (kt >= lo && kt < hi && (!SPLIT || ((kt - lo) & (w.step - 1)) == 0)) {
               if (kt == lo && !(ok = wait_or_abort(&bar.q_full[t], (nq - 1) & 1, abort, lim))) break;
               // the scores before these are in the softmax's registers
               if (c > 0 && !(ok = wait_or_abort(&bar.s_free[t], (c - 1) & 1, abort, lim))) break;
@@ -251,13 +260,13 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         bool ok = true, issued = false;
         Rounds rounds(n_work, blockIdx.x, gridDim.x);
         for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-          const Work w = work_at<KN>(p, wi);
+          const Work w = work_at<KN, SPLIT>(p, wi);
           const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
           issued = true;
           nq += lo < hi;
           for (int kt = w.k_lo; kt < w.k_hi && ok; ++kt, u += 2) {
             if (!(ok = wait_or_abort(&bar.u_full[u % C::kUnits], (u / C::kUnits) & 1, abort, lim))) break;
-            if (kt >= lo && kt < hi) {
+            if (kt >= lo && kt < hi && (!SPLIT || ((kt - lo) & (w.step - 1)) == 0)) {
               const bool first = kt == lo;
               if (first && nq > 1 && !(ok = wait_or_abort(&bar.o_free[t], (nq - 2) & 1, abort, lim))) break;
               const uint64_t vd = vdesc + (((u % C::kUnits) * C::kTile) >> 4);
@@ -291,20 +300,20 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
     const uint32_t ts = tbase + lane_base + t * C::kStride, tp = ts + C::kPCol, to = ts + C::kOCol;
     const float c = p.c;
     const uint64_t c2 = ptx::f2(c, c);
-    int n = 0, no = 0;  // score tiles and items so far
+    int n = 0, no = 0, nb = 0, nj = 0;  // score tiles, items, B's items and joins so far
     bool ok = true;
     Rounds rounds(n_work, blockIdx.x, gridDim.x);
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at<KN>(p, wi);
+      const Work w = work_at<KN, SPLIT>(p, wi);
       const int lo = t ? w.lo[1] : w.lo[0], hi = t ? w.hi[1] : w.hi[0];
       if (lo >= hi) continue;
-      const int tok = w.tok0 + t * tt + row / p.pk;
+      const int tok = (t ? w.tok[1] : w.tok[0]) + row / p.pk;
       // the row's keys [ra, rb)
       int ra = p.window > 0 ? max(0, tok - p.window + 1) : 0, rb = p.causal ? tok + 1 : w.len;
       const bool valid = tok < w.len;
       if (!valid) ra = rb = 0;
       float m = -INFINITY, l = 0.f;
-      for (int kt = lo; kt < hi; ++kt, ++n) {
+      for (int kt = lo; kt < hi; kt += SPLIT ? w.step : 1, ++n) {
         if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.s_full[t], n & 1, abort, lim)))) break;
         ptx::tc_fence_after();
         Scores<KN> s;
@@ -347,18 +356,47 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
         l += ptx::f2_lo(sum) + ptx::f2_hi(sum);
       }
       if (!ok) break;
-      if (!__all_sync(0xffffffffu, wait_or_abort(&bar.o_full[t], no & 1, abort, lim))) {
-        ok = false;
-        break;
+      const bool joined = SPLIT && w.joined();
+      if (joined && t == 1) {
+        // the rows' maxima and sums to A's warps, which read O: once they have
+        // read those of this tile's item before (an item of its own passes at once)
+        if (no > 0 && !(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.o_free[1], (no - 1) & 1, abort, lim)))) break;
+        ++no;
+        join_ml[row] = make_float2(m, l);
+        ptx::mbar_arrive(&bar.join);
+        continue;
       }
+      if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.o_full[t], no & 1, abort, lim)))) break;
       ++no;
+      if (joined) {
+        // B's sums first: then B has left its item before, and the phase of its
+        // o_full that is waited for is the next to complete
+        if (!(ok = __all_sync(0xffffffffu, wait_or_abort(&bar.join, nj & 1, abort, lim) &&
+                                               wait_or_abort(&bar.o_full[1], nb & 1, abort, lim))))
+          break;
+        ++nj;
+      }
+      nb += w.lo[1] < w.hi[1];
       ptx::tc_fence_after();
       const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
       const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
-      store_row<D>(to, l, in, static_cast<__nv_bfloat16*>(p.y) + y0, [&] {
-        ptx::tc_fence_before();
-        ptx::mbar_arrive(&bar.o_free[t]);
-      });
+      __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y0;
+      if (joined) {
+        const float2 o = join_ml[row];
+        const float mm = fmaxf(m, o.x), ref = mm == -INFINITY ? 0.f : mm;
+        const float fa = m == -INFINITY ? 0.f : ptx::ex2((m - ref) * c), fb = o.x == -INFINITY ? 0.f : ptx::ex2((o.x - ref) * c);
+        const float sum = fmaf(l, fa, o.y * fb), inv = sum != 0.f ? 1.f / sum : 0.f;
+        store_joined<D>(to, to + C::kStride, fa * inv, fb * inv, in, y, [&] {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bar.o_free[0]);
+          ptx::mbar_arrive(&bar.o_free[1]);
+        });
+      } else {
+        store_row<D>(to, l, in, y, [&] {
+          ptx::tc_fence_before();
+          ptx::mbar_arrive(&bar.o_free[t]);
+        });
+      }
     }
   }
   ptx::grid_launch_dependents();
@@ -388,7 +426,7 @@ cudaError_t launch(const PackedParams& p, cudaStream_t s) {
       !make_tensor_map_bf16(&kmap, p.k, 4, k_dims, k_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B) ||
       !make_tensor_map_bf16(&vmap, p.v, 4, k_dims, v_str, k_box, CU_TENSOR_MAP_SWIZZLE_128B))
     return cudaErrorInvalidValue;
-  auto k = packed_tc_kernel<D>;
+  auto k = p.ctas ? packed_tc_kernel<D, true> : packed_tc_kernel<D, false>;
   if (cudaError_t e = set_max_dynamic_smem(reinterpret_cast<const void*>(k), C::kSmem); e != cudaSuccess) return e;
   const int64_t work = static_cast<int64_t>(p.max_items) * p.heads;
   PdlLaunch l(dim3(static_cast<unsigned>(work < num_sms() ? work : num_sms())), C::kThreads, C::kSmem, s);

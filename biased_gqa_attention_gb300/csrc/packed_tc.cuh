@@ -25,21 +25,24 @@ __device__ __forceinline__ bool wait_or_abort(uint64_t* bar, uint32_t parity, vo
 }
 
 // One entry of the work list for one head group: two query tiles of
-// tile_tok / 2 tokens each.
+// tile_tok / 2 tokens each, or (split) one query tile twice, A with every other
+// key tile and B with the rest.
 struct Work {
-  int row0, len, tok0, h0, hk;
-  int lo[2], hi[2];  // key tiles (of KN keys) of query tiles A and B (empty: tile B has no tokens)
-  int k_lo, k_hi;    // their union
+  int row0, len, h0, hk;
+  int tok[2];        // first token of query tiles A and B
+  int lo[2], hi[2];  // their key tiles (of KN keys), every `step`-th (empty: tile B has no tokens, or no keys)
+  int k_lo, k_hi;    // all key tiles
+  int step;          // 1, or 2: split
+  __device__ __forceinline__ bool joined() const { return step == 2 && lo[1] < hi[1]; }
 };
 
-template <int KN>
+template <int KN, bool SPLIT>
 __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
   Work r;
   const int64_t at = w / p.heads;
   const PackedItem it = p.items[at];
   r.row0 = it.row0;
   r.len = it.len;
-  r.tok0 = it.tok0;
   r.h0 = static_cast<int>(w - at * p.heads) * p.pk;
   r.hk = r.h0 / p.g;
   const int tt = p.tile_tok / 2;
@@ -47,7 +50,8 @@ __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
   r.k_hi = 0;
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
-    const int t0 = it.tok0 + t * tt, t1 = min(it.len, t0 + tt);
+    const int t0 = it.tok0 + (SPLIT && it.split ? 0 : t * tt), t1 = min(it.len, t0 + tt);
+    r.tok[t] = t0;
     r.lo[t] = r.hi[t] = 0;
     if (t0 < t1) {
       r.lo[t] = (p.window > 0 ? max(0, t0 - p.window + 1) : 0) / KN;
@@ -55,6 +59,14 @@ __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
       r.k_lo = min(r.k_lo, r.lo[t]);
       r.k_hi = max(r.k_hi, r.hi[t]);
     }
+  }
+  r.step = SPLIT && it.split ? 2 : 1;
+  if (r.step == 2) {
+    const int n = r.k_hi - r.k_lo;
+    r.lo[1] = r.k_lo + 1;
+    r.hi[0] = r.k_lo + ((n - 1) | 1);       // behind A's last: tiles 0, 2, .. below n
+    r.hi[1] = r.k_lo + (n / 2) * 2;         // behind B's last: tiles 1, 3, .. below n
+    if (n < 2) r.lo[1] = r.hi[1] = 0;
   }
   return r;
 }
@@ -177,6 +189,33 @@ __device__ __forceinline__ void store_row(uint32_t to, float l, bool in, __nv_bf
           v[e] = ptx::pack_bf16x2(__uint_as_float(o[k >> 5][k & 31]) * inv, __uint_as_float(o[k >> 5][(k & 31) + 1]) * inv);
         }
         *reinterpret_cast<uint4*>(y + 64 * q + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
+    }
+  }
+}
+
+// The same for a row whose keys are in two parts: O at `ta` times fa and at `tb` times fb.
+template <int D, class F>
+__device__ __forceinline__ void store_joined(uint32_t ta, uint32_t tb, float fa, float fb, bool in, __nv_bfloat16* y,
+                                             F release) {
+#pragma unroll
+  for (int q = 0; q < D / 32; ++q) {
+    uint32_t a[32], b[32];
+    ptx::tmem_ld32(ta + 32 * q, a);
+    ptx::tmem_ld32(tb + 32 * q, b);
+    ptx::tmem_wait_ld();
+    if (q == D / 32 - 1) release();
+    if (in) {
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int k = 8 * x + 2 * e;
+          v[e] = ptx::pack_bf16x2(fmaf(__uint_as_float(b[k]), fb, __uint_as_float(a[k]) * fa),
+                                  fmaf(__uint_as_float(b[k + 1]), fb, __uint_as_float(a[k + 1]) * fa));
+        }
+        *reinterpret_cast<uint4*>(y + 32 * q + 8 * x) = make_uint4(v[0], v[1], v[2], v[3]);
       }
     }
   }

@@ -111,7 +111,6 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
   const uint32_t tbase = bar.tmem_base;
   ptx::grid_dependency_wait();
   const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
-  const int tt = p.tile_tok / 2;
   Rounds rounds(n_work, blockIdx.x / 2, gridDim.x / 2);
   int armed[2] = {0, 0};  // warp 0: units whose barriers expect bytes
   uint32_t tails = 0;  // warp 0: phase of each unit's v_land
@@ -150,14 +149,14 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       return true;
     };
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at<kBN>(p, wi);
+      const Work w = work_at<kBN, false>(p, wi);
       const bool active = rank ? w.lo[1] < w.hi[1] : w.lo[0] < w.hi[0];
       if (active) {
         if (lane == 0) {
           ok = !nq || wait_or_abort(&bar.q_empty, (nq - 1) & 1, abort, lim);
           if (ok) {
             ptx::mbar_arrive_expect_tx(&bar.q_full, kQBytes);
-            ptx::tma_load_4d(sm, &qmap, &bar.q_full, 0, w.h0, w.row0 + w.tok0 + rank * tt, 0);
+            ptx::tma_load_4d(sm, &qmap, &bar.q_full, 0, w.h0, w.row0 + (rank ? w.tok[1] : w.tok[0]), 0);
           }
         }
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -185,7 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       int u = 0, nq = 0, c = 0;  // units of its kind, items, products so far
       bool ok = true, issued = false;
       for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-        const Work w = work_at<kBN>(p, wi);
+        const Work w = work_at<kBN, false>(p, wi);
         const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
         issued = true;
         nq += lo < hi;
@@ -246,10 +245,10 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
     int n = 0, no = 0;
     bool ok = true;
     for (int64_t wi; ok && (wi = rounds.next()) >= 0;) {
-      const Work w = work_at<kBN>(p, wi);
+      const Work w = work_at<kBN, false>(p, wi);
       const int lo = rank ? w.lo[1] : w.lo[0], hi = rank ? w.hi[1] : w.hi[0];
       if (lo >= hi) continue;
-      const int tok = w.tok0 + rank * tt + row / p.pk;
+      const int tok = (rank ? w.tok[1] : w.tok[0]) + row / p.pk;
       const bool valid = tok < w.len;
       int ra = p.window > 0 ? max(0, tok - p.window + 1) : 0, rb = p.causal ? tok + 1 : w.len;
       if (!valid) ra = rb = 0;

@@ -107,6 +107,19 @@ CASES = [
     (tuple((53 * i) % 40 for i in range(300)), 4, 2, 128, torch.bfloat16, True, 0, False, 0, 0),
     (tuple(1 for i in range(1500)), 2, 1, 64, torch.bfloat16, True, 0, False, 0, 0),
     (tuple((53 * i) % 40 for i in range(100)), 4, 2, 64, torch.float32, True, 9, False, 0, 7),
+    # long prompts in small batches: their keys split over a CTA's two query tiles
+    ((257,), 2, 1, 128, torch.bfloat16, True, 0, False, 0, 0),
+    ((481, 1, 640), 4, 2, 128, torch.bfloat16, True, 0, True, 5, 9),
+    ((1000, 7, 399), 4, 4, 128, torch.bfloat16, False, 0, False, 0, 0),
+    ((1601, 129), 2, 2, 128, torch.bfloat16, True, 450, False, 0, 3),
+    ((385, 900), 4, 2, 64, torch.bfloat16, True, 0, True, 1, 1),
+    ((1025, 513), 6, 2, 64, torch.bfloat16, False, 600, False, 0, 0),
+    ((700,), 16, 1, 64, torch.bfloat16, True, 0, False, 0, 0),
+    # more tiles than CTAs: no splits
+    (EDGES + (600,), 64, 64, 128, torch.bfloat16, True, 0, False, 2, 2),
+    (EDGES + (600,), 64, 64, 64, torch.bfloat16, True, 0, True, 0, 0),
+    (EDGES + (600,), 64, 64, 64, torch.bfloat16, False, 200, False, 0, 0),
+    (EDGES + (600,), 128, 64, 128, torch.bfloat16, True, 300, False, 0, 0),
 ]
 
 
@@ -226,7 +239,7 @@ def test_a_wait_that_runs_out_is_reported(D):
     check(y, ref, tol, "after")
 
 
-@pytest.mark.parametrize("D,window", [(256, 90), (256, 0), (128, 90), (64, 0)])
+@pytest.mark.parametrize("D,window", [(256, 90), (256, 0), (128, 90), (64, 0), (128, 0)])
 def test_the_same_bits_from_cold_and_warm_caches(D, window):
     """Copies that land late, early and in other orders (L2 full of other data, or
     of this) change no bit."""
