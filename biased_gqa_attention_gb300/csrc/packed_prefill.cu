@@ -23,7 +23,7 @@ __device__ __forceinline__ int item_cost(const PackedParams& p, int len, int tok
 }
 
 // One CTA.  A causal prompt's tiles cost from one to len / 128 key tiles, so the
-// list is sorted by cost, dearest first (a counting sort over 1024 cost
+// list is sorted by cost, dearest first (a counting sort over kPlanThreads cost
 // classes): CTAs that take items in turn then end together.  The order within a
 // class follows the atomics; every item is computed alone, so no result
 // depends on it.  Also checks cu_seqlens: a bad one leaves an empty list.
@@ -36,8 +36,8 @@ __device__ __forceinline__ int item_cost(const PackedParams& p, int len, int tok
 // of 64, 55 and 42; twelve of 1 to 2047, 8 heads of 128, 38.2 and 36.4; four of 900,
 // 27 and 25 (splitting from one share on: 31).
 __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedParams p) {
-  __shared__ int hist[1024];
-  __shared__ int warp_sum[32];
+  __shared__ int hist[kPlanThreads];
+  __shared__ int warp_sum[kPlanThreads / 32];
   __shared__ int bad;
   __shared__ unsigned long long total_s;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     }
     return;
   }
-  const float to_class = 1023.f / static_cast<float>(p.T / 128 + 2);  // an item's cost is below that
+  const float to_class = static_cast<float>(kPlanThreads - 1) / static_cast<float>(p.T / 128 + 2);  // an item's cost is below that
   int64_t limit = INT_MAX;  // items that cost more are split
   // Passes over all tiles: the total cost, the classes' sizes, the items.  One loop
   // (not unrolled), since the kernel's time is mostly fetching its code.
@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
 #pragma unroll 1
         for (int end = min(len, tok + p.tile_tok); tok < end; tok += tokens) {
           if (split) cost = (item_cost(p, len, tok, tokens) + 1) / 2;
-          const int at = atomicAdd(&hist[1023 - min(1023, static_cast<int>(cost * to_class))], 1);
+          const int at = atomicAdd(&hist[kPlanThreads - 1 - min(kPlanThreads - 1, static_cast<int>(cost * to_class))], 1);
           if (pass == 2 && at < p.max_items && EXTKV_IN(at, 1, p.max_items, p.status))
             p.items[at] = PackedItem{row0, len, tok, split};
         }
