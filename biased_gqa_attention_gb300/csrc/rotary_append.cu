@@ -387,11 +387,13 @@ cudaError_t launch_rotary(const RotaryArgs& a) {
   p.status = a.status;
   // Few rows: a CTA per row and per some of its heads, so that a decode step's
   // few hundred kilobytes spread over the GPU (each CTA computes its row's
-  // angles again); many rows: as many rows a CTA as make one wave of CTAs.
+  // angles again), as long as they make one wave: 300 rows of 10 heads of 128 take
+  // 8 us so, 10 with CTAs for more than one wave, 50 rows of 72 heads of 256 8 and 10.
+  // Many rows: as many rows a CTA as make one wave of CTAs.
   const int heads = a.q.heads + a.k.heads + a.v.heads;
   const int64_t ctas = int64_t(num_sms()) * kMinCtas;
   int hpc = std::min(heads, kMaxHeadsPerCta);
-  while (hpc > 4 && p.n_rows * ((heads + hpc - 1) / hpc) < ctas) hpc = (hpc + 1) / 2;
+  while (hpc > 4 && 2 * p.n_rows * ((heads + hpc - 1) / hpc) <= ctas) hpc = (hpc + 1) / 2;
   const int64_t rpc = hpc == heads ? std::min<int64_t>(kMaxRows, (p.n_rows + ctas - 1) / ctas) : 1;
   const int64_t gx = (p.n_rows + rpc - 1) / rpc;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
