@@ -443,7 +443,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (groups) look_up();
     int g = 0, slot = 0, phase = 1;  // phase: of the empty barrier to wait for (none in the first round)
     uint32_t idle = 0;
-    while (__any_sync(0xffffffffu, g < groups)) {
+    bool stop = false;
+    while (!stop && __any_sync(0xffffffffu, g < groups)) {
       const bool can = g < groups && (g < NS || ptx::mbar_test_wait(&empty[mine][slot], phase));
       if (can) {
         const CUtensorMap* map = (g & 1) ? &vmap : &kmap;
@@ -492,11 +493,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       idle = __any_sync(0xffffffffu, can) ? 0 : idle + 1;
       if (idle > p.wait_limit) *abort = 1;
-      if (*abort) break;
+      // a vote: a consumer may set the flag between two lanes' reads, and the
+      // votes above need all lanes until all leave
+      stop = __any_sync(0xffffffffu, *abort != 0);
     }
-    if (*abort) {  // copies still in flight land before the CTA leaves
-      for (int x = g > NS ? g - NS : 0; x < g; ++x) ptx::mbar_wait_bounded(&full[mine][x % NS], (x / NS) & 1, kWaitPolls >> 6);
-    }
+    // Each slot's newest copy lands before the CTA leaves, also where a consumer gives
+    // up only after this (its copies are the ones that it no longer waits for).
+    for (int x = g > NS ? g - NS : 0; x < g; ++x) ptx::mbar_wait_bounded(&full[mine][x % NS], (x / NS) & 1, kWaitPolls >> 6);
     __syncwarp();
   } else {
     // ---------------- consumers ----------------
