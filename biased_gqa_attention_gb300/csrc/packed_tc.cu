@@ -205,12 +205,16 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
           ++u;
         }
       }
-      if (lane == 0 && *abort) {  // copies still in flight land before the CTA leaves
-        for (int x = u >= C::kUnits ? u - C::kUnits + 1 : 0; x <= u; ++x)
+      // Copies still in flight land before the CTA leaves, also where another warp
+      // gives up only after this: the newest of each slot and of Q, and where
+      // this warp gave up the unit it stood at, which may have been sent.
+      if (lane == 0) {
+        const int sent = ok ? u : u + 1;
+        for (int x = sent > C::kUnits ? sent - C::kUnits : 0; x < sent; ++x)
           ptx::mbar_wait_bounded(&bar.u_full[x % C::kUnits], (x / C::kUnits) & 1, kWaitPolls >> 6);
         for (int t = 0; t < 2; ++t)
           if (nq[t]) ptx::mbar_wait_bounded(&bar.q_full[t], (nq[t] - 1) & 1, kWaitPolls >> 6);
-        ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
+        if (!ok) ptx::mbar_wait_bounded(&bar.v_tail, tails & 1, kWaitPolls >> 6);
       }
       __syncwarp();
     } else if (warp < 3) {

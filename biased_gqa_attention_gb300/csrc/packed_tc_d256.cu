@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
         load(true, w, kt);
       }
     }
-    if (lane == 0 && *abort && nq) ptx::mbar_wait_bounded(&bar.q_full, (nq - 1) & 1, kWaitPolls >> 6);
+    // (the copy of Q lands before the CTA leaves, also where another warp gives up only after this)
+    if (lane == 0 && nq) ptx::mbar_wait_bounded(&bar.q_full, (nq - 1) & 1, kWaitPolls >> 6);
     __syncwarp();
   } else if (warp < 3) {
     // ---------------- MMAs: Q K^T (warp 1), P V (warp 2) ----------------

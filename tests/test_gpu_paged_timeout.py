@@ -11,6 +11,7 @@ import pytest
 import torch
 
 from biased_gqa_attention_gb300 import extkv as ek
+import test_gpu_packed_prefill as packed
 import test_gpu_paged_decode as paged
 
 pytestmark = pytest.mark.gpu
@@ -61,3 +62,20 @@ def test_paged_decode_gives_up_cleanly(lens, Hq, Hkv, D, page, algo):
         y, st = torch.empty_like(good), ek.new_status()
         give_up(lambda: ek.attention_paged_decode(y, q, k, v, table, nonpad, scale, status=st), st, y, good,
                 (lens, D, algo))
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,window", [
+    ((20,), 4, 2, 64, 0),
+    ((1, 0, 129, 700), 8, 4, 128, 0),
+    ((2047,), 8, 4, 128, 0),                # items whose keys are split over the CTA's two query tiles
+    ((900, 33, 128), 4, 2, 64, 100),
+    ((5,), 2, 1, 256, 0),
+    ((700, 1, 300), 4, 2, 256, 200),
+], ids=lambda x: str(x))
+def test_packed_prefill_gives_up_cleanly(lens, Hq, Hkv, D, window):
+    scale = 1.0 / math.sqrt(D)
+    q, k, v, cu = packed.make(lens, Hq, Hkv, D, torch.bfloat16)
+    good = packed.run(q, k, v, cu, scale, True, window)
+    assert ek.extkv_last_kernel() == "packed_tcgen05"
+    y, st = torch.empty_like(good), ek.new_status()
+    give_up(lambda: ek.attention_packed_prefill(y, q, k, v, cu, scale, window=window, status=st), st, y, good, (lens, D))
