@@ -793,17 +793,15 @@ __global__ void __launch_bounds__(Cfg<DK, DV, MODE>::kThreads, 1)
           else if (is_v && j + 1 < T) ok = load_term(j + 1);
         }
       }
-      // copies still in flight after an abort land before the CTA leaves
-      if (*abort) {
-        if (C::kQSmem) ptx::mbar_wait_bounded(&bar.q_full, 0, kWaitPolls);
-        for (int u = issued > C::kNU ? issued - C::kNU : 0; u < issued; ++u)
-          ptx::mbar_wait_bounded(&bar.u_full[u % C::kNU], (u / C::kNU) & 1, kWaitPolls);
-        if (C::kTerm)
-          for (int j = t_issued > C::kTB ? t_issued - C::kTB : 0; j < t_issued; ++j)
-            ptx::mbar_wait_bounded(&bar.t_full[j % C::kTB], (j / C::kTB) & 1, kWaitPolls);
-      } else if (C::kQSmem && T == 0) {
-        ptx::mbar_wait_bounded(&bar.q_full, 0, kWaitPolls);  // no consumer: let it land
-      }
+      // Copies still in flight land before the CTA leaves (the newest of each
+      // buffer): of a query tile without keys, which has no consumer, and of an
+      // abort, which another warp may enter only after this.
+      if (C::kQSmem) ptx::mbar_wait_bounded(&bar.q_full, 0, kWaitPolls);
+      for (int u = issued > C::kNU ? issued - C::kNU : 0; u < issued; ++u)
+        ptx::mbar_wait_bounded(&bar.u_full[u % C::kNU], (u / C::kNU) & 1, kWaitPolls);
+      if (C::kTerm)
+        for (int j = t_issued > C::kTB ? t_issued - C::kTB : 0; j < t_issued; ++j)
+          ptx::mbar_wait_bounded(&bar.t_full[j % C::kTB], (j / C::kTB) & 1, kWaitPolls);
     }
   } else if (warp == 1) {
     // ---------------- MMA issuer ----------------
@@ -1341,9 +1339,9 @@ __global__ void __launch_bounds__(Cfg<DK, DV, MODE>::kThreads, 1)
     }
   }
   ptx::grid_launch_dependents();
-  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);
   ptx::tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);  // every warp has given up or is done
   ptx::tc_fence_after();
   if (warp == 1) ptx::tmem_dealloc(tbase, C::kTmemCols);
 }

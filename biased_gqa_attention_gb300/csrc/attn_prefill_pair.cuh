@@ -557,9 +557,9 @@ __global__ void __launch_bounds__(PairCfg<MODE>::kThreads, 1)
     __syncwarp();
   }
   ptx::grid_launch_dependents();
-  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);
   ptx::tc_fence_before();
   __syncthreads();
+  if (tid == 0 && *abort) report(p.status, EXTKV_DEV_TIMEOUT);  // every warp has given up or is done
   __syncwarp();
   // neither CTA leaves (or frees tensor memory) while the other may still
   // signal it or read its shared memory
