@@ -177,6 +177,30 @@ def _need(t, name, dims=None, dtype=None):
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
 
 
+_recording = {}  # stream handle of each open StepRecorder -> the workspaces its step needs
+
+
+def _need_workspace(workspace, need, device, stream):
+    """The caller's workspace, or one from the pool of the stream the call runs
+    on (memory that is given back while the kernels run is then reused behind
+    them).  One for a call that is being recorded stays with its step, which
+    uses it again at every launch."""
+    if workspace is None:
+        if not need:
+            return None
+        handle = _stream(stream) or 0
+        if handle == torch.cuda.current_stream().cuda_stream:
+            workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        else:
+            with torch.cuda.stream(torch.cuda.ExternalStream(handle)):
+                workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        if handle in _recording:
+            _recording[handle].append(workspace)
+        return workspace
+    _need(workspace, "workspace")
+    return workspace
+
+
 @dataclass
 class BiasSpec:
     """extkv_bias_spec: causal + sliding window + image spans + padding, with an
@@ -266,8 +290,7 @@ def _marshal_attention(y, q, k_cache, v_cache, nonpad, scale, bias, fused, works
     c = None if fused is None else fused._c()
     if workspace is None:
         need = attention_ext_kv_workspace_size(B, Hq, Hkv, S_q, max_seq, D, q.dtype, Dv)
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _need_workspace(None, need, q.device, stream)
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     lib = load()
     keep = (c, workspace, y, q, k_cache, v_cache, bias, nonpad, status)
@@ -335,8 +358,7 @@ def _marshal_attention_scatter(y, q, k_cache, v_cache, k_new, v_new, write_idx, 
     c = None if fused is None else fused._c()
     if workspace is None:
         need = load().attention_ext_kv_workspace_size(B, Hq, Hkv, S_q, max_seq, D, _dt(q))
-        if need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        workspace = _need_workspace(None, need, q.device, stream)
     ws = 0 if workspace is None else workspace.numel() * workspace.element_size()
     keep = (c, workspace, y, q, k_cache, v_cache, k_new, v_new, write_idx, bias, nonpad, status)
     return load().attention_ext_kv_scatter, (_p(y), _p(q), _p(k_cache), _p(v_cache), _p(k_new), _p(v_new),
@@ -564,22 +586,6 @@ def attention_paged_decode_workspace_size(B, Hq, Hkv, D, dtype) -> int:
     return int(load().attention_paged_decode_workspace_size(B, Hq, Hkv, D, dt))
 
 
-def _need_workspace(workspace, need, device, stream):
-    """The caller's workspace, or one from the pool of the stream the call runs
-    on (memory that is given back while the kernels run is then reused behind
-    them)."""
-    if workspace is None:
-        if not need:
-            return None
-        handle = _stream(stream)
-        if handle == torch.cuda.current_stream().cuda_stream:
-            return torch.empty(need, dtype=torch.uint8, device=device)
-        with torch.cuda.stream(torch.cuda.ExternalStream(handle or 0)):
-            return torch.empty(need, dtype=torch.uint8, device=device)
-    _need(workspace, "workspace")
-    return workspace
-
-
 def _ws_bytes(workspace) -> int:
     return 0 if workspace is None else workspace.numel() * workspace.element_size()
 
@@ -613,8 +619,8 @@ def attention_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, wi
     """Attention of one new token per sequence, q (B,Hq,D), over its first
     ``nonpad[b]`` slots (the last ``window`` of them when window > 0) in the
     pages (num_pages,Hkv,page_size,D); writes ``y`` (B,Hq,D).  The workspace is
-    allocated here when not given (a call that is recorded into a step needs one
-    that lives as long as the step)."""
+    allocated here when not given (and stays with the step where the call is
+    recorded into one)."""
     fn, args, _ = _marshal_paged_decode(y, q, k_pages, v_pages, page_table, nonpad, scale, window, workspace, status,
                                         stream)
     _check(fn(*args))
@@ -666,8 +672,7 @@ def attention_packed_prefill(y, q, k, v, cu_seqlens, scale, causal: bool = True,
     k, v (T,Hkv,D), sequence b in rows cu_seqlens[b]..cu_seqlens[b+1]-1; writes
     the sequences' rows of ``y`` (T,Hq,D).  q, k and v may have any row stride
     that is a multiple of 16 bytes.  The workspace is allocated here when not
-    given (a call that is recorded into a step needs one that lives as long as
-    the step)."""
+    given (and stays with the step where the call is recorded into one)."""
     fn, args, _ = _marshal_packed_prefill(y, q, k, v, cu_seqlens, scale, causal, window, workspace, status, stream)
     _check(fn(*args))
 
@@ -754,15 +759,20 @@ class use_algo:
 class RecordedStep:
     """A step recorded with StepRecorder: calling it starts every recorded
     library call again with one launch, on ``stream`` (a torch stream or a raw
-    handle; default the current stream)."""
+    handle; default the current stream).  It keeps the workspaces that its calls
+    allocated; the tensors they were given must stay alive and in place."""
 
-    __slots__ = ("_h",)
+    __slots__ = ("_h", "_workspaces")
 
-    def __init__(self, handle: int):
+    def __init__(self, handle: int, workspaces=()):
         self._h = ctypes.c_void_p(handle)
+        self._workspaces = list(workspaces)
 
     def __call__(self, stream=None):
-        code = load().extkv_step_launch(self._h, _stream(stream))
+        handle = _stream(stream)
+        for w in self._workspaces:  # freed with the step, reused only behind this launch
+            w.record_stream(torch.cuda.ExternalStream(handle or 0))
+        code = load().extkv_step_launch(self._h, handle)
         if code != EXTKV_OK:
             raise ExtKVError(code, load().extkv_last_error().decode())
 
@@ -782,15 +792,17 @@ class StepRecorder:
         _check(load().extkv_step_begin(ctypes.byref(h)))
         self.stream = h.value
         self.step = None
+        _recording[self.stream] = []
         return self
 
     def __exit__(self, exc_type, exc, tb):
         out = ctypes.c_void_p()
+        workspaces = _recording.pop(self.stream, ())
         code = load().extkv_step_end(ctypes.c_void_p(self.stream), ctypes.byref(out))
         if exc_type is not None:
             if out.value:
                 load().extkv_step_free(out)
             return False
         _check(code)
-        self.step = RecordedStep(out.value)
+        self.step = RecordedStep(out.value, workspaces)
         return False
