@@ -1275,7 +1275,8 @@ template <class C>
 int cluster_size(const PagedParams& p, bool forced) {
   const int64_t units = static_cast<int64_t>(p.B) * p.units;
   const int64_t cap = static_cast<int64_t>(p.max_pages) * p.page_size;
-  const int64_t keys = p.window > 0 && p.window + C::KT < cap ? p.window + C::KT : cap;
+  const int64_t in_window = static_cast<int64_t>(p.window) + C::KT;  // windows go up to 2^31 - 1
+  const int64_t keys = p.window > 0 && in_window < cap ? in_window : cap;
   const double longest = static_cast<double>(keys) * C::D * 4;  // bytes of a unit
   const void* k = reinterpret_cast<const void*>(paged_decode_mma_kernel<C>);
   for (int c = kMaxCluster; c > 1; c /= 2) {
