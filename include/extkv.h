@@ -23,6 +23,12 @@
  *     tensor maps are keyed by pointer values and never dereferenced.
  *     Structs passed by pointer (extkv_bias_spec) are HOST memory, read
  *     during the call only.
+ *   - One GPU: every device pointer lies in the own memory of the current
+ *     device, where the call launches (cudaMalloc or a pool of it: not a peer's
+ *     memory, not managed and not host memory).  Some kernels fetch the bias
+ *     (decode on clusters) or k and v (packed prefill at head size 256) by
+ *     multicast copies, which are for such memory, in programs that run on one
+ *     GPU alone: the library is not for jobs over several GPUs.
  *   - Every call is asynchronous on `stream` (a cudaStream_t passed as void*;
  *     NULL is the legacy default stream) and never synchronises, except
  *     extkv_read_status.
