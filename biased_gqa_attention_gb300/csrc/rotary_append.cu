@@ -10,8 +10,9 @@
 // only the fraction of a turn matters.  F = frac(inv_freq / 2 pi) as a 128-bit
 // fixed-point number (inv_freq is 24 bits times a power of two, so this is one
 // integer product with the first 96 bits of 1 / 2 pi); position * F wraps as
-// angles wrap at a turn, and errs by |position * inv_freq| * 2^-95 turns at
-// most.  The upper 64 bits, a signed fraction, go to sincospif.  No fp64.
+// angles wrap at a turn.  The upper 64 bits, a signed fraction, go to sincospif.
+// Cut off are 2^-96 of a turn and less per radian (1 / 2 pi), less than 2^-128
+// per position (F) and less than 2^-64 (the lower 64 bits).  No fp64.
 #include <algorithm>
 
 #include "common.cuh"

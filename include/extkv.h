@@ -347,8 +347,9 @@ int attention_ext_kv_noalloc(void *y, const void *q, const void *k_cache, const 
  * (i, i + rotary_dim/2), or (2i, 2i + 1) when `interleaved` is not 0:
  *     (a, b) -> (a cos - b sin, b cos + a sin)
  * The other elements pass unchanged.  Far positions lose nothing: the angle is
- * formed in fixed-point turns, which wrap as angles do, and errs by
- * |position * inv_freq| * 2^-95 turns at most before it is rounded to fp32;
+ * formed in fixed-point turns, which wrap as angles do, and errs by less than
+ *     2^-64 + |position| * 2^-128 + |position * inv_freq| * 2^-96 turns
+ * before it is rounded to fp32 (so an angle below 2^-64 turns counts as 0);
  * sine, cosine and the turn are fp32, rounded once to the element type.
  * |inv_freq| < 2^32 (a pair of any other frequency becomes NaN).
  * n_axes is 1 to 4; the sections sum to rotary_dim / 2; rotary_dim is even,
