@@ -58,15 +58,30 @@ __device__ __forceinline__ void report(int32_t* status, int32_t flag) {
 // flagged in the status word (a bounds check in place of a sanitizer: no trap,
 // no fault).  Otherwise the test is the constant true and its arguments are
 // not evaluated.
+// EXTKV_IN_KIND also leaves in status[3] what kind of buffer was tested, so that a
+// run can tell that its tests were made at all.
+enum : int32_t {
+  kChkLens = 0x1,     // nonpad, cu_seqlens, write_idx
+  kChkTable = 0x2,    // the page table
+  kChkRows = 0x4,     // rows of q, k, v read
+  kChkPages = 0x8,    // rows of the pools, read or written
+  kChkOut = 0x10,     // rows of y, q_out, k_out
+  kChkPartial = 0x20, // tile counts and partials in the workspace
+  kChkItems = 0x40,   // the list of query tiles
+  kChkAngles = 0x80,  // positions and frequencies
+};
 #ifdef EXTKV_CHECKED
-__device__ __forceinline__ bool in_bounds(int64_t first, int64_t count, int64_t n, int32_t* status) {
+__device__ __forceinline__ bool in_bounds(int64_t first, int64_t count, int64_t n, int32_t* status, int32_t kind = 0) {
+  if (status && kind && !(*static_cast<volatile int32_t*>(status + 3) & kind)) atomicOr(status + 3, kind);
   if (first >= 0 && count >= 0 && first + count <= n) return true;
   report(status, EXTKV_DEV_BOUNDS);
   return false;
 }
 #define EXTKV_IN(first, count, n, status) ::extkv::in_bounds((first), (count), (n), (status))
+#define EXTKV_IN_KIND(kind, first, count, n, status) ::extkv::in_bounds((first), (count), (n), (status), (kind))
 #else
 #define EXTKV_IN(first, count, n, status) true
+#define EXTKV_IN_KIND(kind, first, count, n, status) true
 #endif
 
 // ---- the bias specification, evaluated on the device -----------------------

@@ -35,6 +35,14 @@ struct PackedParams {
   uint32_t wait_limit;
 };
 
+// Checked builds: cu_seqlens[b], item `at` of the list.
+__device__ __forceinline__ bool cu_in(const PackedParams& p, int64_t b) {
+  return EXTKV_IN_KIND(kChkLens, b, 1, static_cast<int64_t>(p.B) + 1, p.status);
+}
+__device__ __forceinline__ bool item_in(const PackedParams& p, int64_t at) {
+  return EXTKV_IN_KIND(kChkItems, at, 1, p.max_items, p.status);
+}
+
 // The keys some of `tokens` rows from tok0 on attends, [lo, hi).
 __device__ __forceinline__ int2 item_keys(const PackedParams& p, int len, int tok0, int tokens) {
   const int last = min(len, tok0 + tokens);

@@ -51,6 +51,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
   __syncthreads();
   bool mine_bad = false;
   for (int64_t b = tid; b <= p.B; b += kPlanThreads) {
+    if (!cu_in(p, b)) break;
     const int64_t x = p.cu[b];
     mine_bad |= x < 0 || x > p.T || (b > 0 && p.cu[b - 1] > x);
   }
@@ -73,6 +74,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
     // a warp per sequence, a lane per tile
 #pragma unroll 1
     for (int b = warp; b < p.B; b += kPlanThreads / 32) {
+      if (!(cu_in(p, b) && cu_in(p, b + 1))) break;
       const int row0 = static_cast<int>(p.cu[b]), len = static_cast<int>(p.cu[b + 1]) - row0;
 #pragma unroll 1
       for (int64_t t = static_cast<int64_t>(lane) * p.tile_tok; t < len; t += 32 * p.tile_tok) {
@@ -88,7 +90,7 @@ __global__ void __launch_bounds__(kPlanThreads) packed_plan_kernel(const PackedP
         for (int end = min(len, tok + p.tile_tok); tok < end; tok += tokens) {
           if (split) cost = (item_cost(p, len, tok, tokens) + 1) / 2;
           const int at = atomicAdd(&hist[kPlanThreads - 1 - min(kPlanThreads - 1, static_cast<int>(cost * to_class))], 1);
-          if (pass == 2 && at < p.max_items && EXTKV_IN(at, 1, p.max_items, p.status))
+          if (pass == 2 && at < p.max_items && item_in(p, at))
             p.items[at] = PackedItem{row0, len, tok, split};
         }
       }
@@ -155,10 +157,14 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
   float* ps = qs + kRows * D;
   const int chunks = D * static_cast<int>(sizeof(T)) / 16;
   const int64_t n_work = static_cast<int64_t>(*p.count) * p.heads;
+  // elements of a tensor of T rows (checked builds)
+  [[maybe_unused]] auto rows_of = [&](int64_t row_stride, int heads) {
+    return (p.T - 1) * row_stride + static_cast<int64_t>(heads) * D;
+  };
   SimtState<DPL> st;
   for (int64_t w = blockIdx.x; w < n_work; w += gridDim.x) {
     const int64_t at = w / p.heads;
-    if (!EXTKV_IN(at, 1, p.max_items, p.status)) break;
+    if (!item_in(p, at)) break;
     const PackedItem item = p.items[at];
     const int h0 = static_cast<int>(w - at * p.heads) * p.pk, hk = h0 / p.g;
     const int2 keys = item_keys(p, item.len, item.tok0, p.tile_tok);
@@ -168,8 +174,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
       const uint32_t kd = ptx::smem_u32(ring + s * stage), vd = kd + KT * stride * sizeof(T);
       for (int x = tid; x < KT * chunks; x += kWarps * 32) {
         const int r = x / chunks, ch = x - r * chunks;
-        const bool in = k0 + r < keys.y;  // keys past the range are filled with zeros
+        bool in = k0 + r < keys.y;  // keys past the range are filled with zeros
         const int64_t row = in ? item.row0 + k0 + r : 0;
+        in = in && EXTKV_IN_KIND(kChkRows, row * p.k_stride + hk * D, D, rows_of(p.k_stride, p.Hkv), p.status) &&
+             EXTKV_IN_KIND(kChkRows, row * p.v_stride + hk * D, D, rows_of(p.v_stride, p.Hkv), p.status);
         const uint32_t to = r * stride * sizeof(T) + ch * 16;
         cp_async_16(kd + to, reinterpret_cast<const uint8_t*>(static_cast<const T*>(p.k) + row * p.k_stride + hk * D) + ch * 16,
                     in ? 16 : 0);
@@ -182,9 +190,10 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
     cp_async_commit();
     simt_stage_q<T, DPL>(qs, D, p.c, [&](int r) -> const T* {
       const int row = warp * kRows + r, tok = item.tok0 + row / p.pk;
-      return tok < item.len ? static_cast<const T*>(p.q) + (item.row0 + tok) * p.q_stride +
-                                  static_cast<int64_t>(h0 + row % p.pk) * D
-                            : nullptr;
+      const int64_t q_at = (item.row0 + tok) * p.q_stride + static_cast<int64_t>(h0 + row % p.pk) * D;
+      return tok < item.len && EXTKV_IN_KIND(kChkRows, q_at, D, rows_of(p.q_stride, p.Hq), p.status)
+                 ? static_cast<const T*>(p.q) + q_at
+                 : nullptr;
     });
     for (int t = 0; t < nt; ++t) {
       if (t + 1 < nt) load(t + 1, (t + 1) & 1);
@@ -215,7 +224,7 @@ __global__ void __launch_bounds__(kWarps * 32, 1) packed_simt_kernel(const Packe
         const float inv = st.l[r] != 0.f ? 1.f / st.l[r] : 0.f;
         const int64_t y0 = (static_cast<int64_t>(item.row0 + tok) * p.Hq + h0 + row % p.pk) * D;
         T* y = static_cast<T*>(p.y);
-        if (EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status)) {
+        if (EXTKV_IN_KIND(kChkOut, y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status)) {
 #pragma unroll
           for (int i = 0; i < DPL; ++i) {
             const int d = lane + 32 * i;

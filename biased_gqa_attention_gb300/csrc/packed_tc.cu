@@ -383,7 +383,7 @@ __global__ void __launch_bounds__(Cfg<D>::kThreads, 1)
       nb += w.lo[1] < w.hi[1];
       ptx::tc_fence_after();
       const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
-      const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
+      const bool in = valid && EXTKV_IN_KIND(kChkOut, y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
       __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y0;
       if (joined) {
         const float2 o = join_ml[row];

@@ -40,7 +40,7 @@ template <int KN, bool SPLIT>
 __device__ __forceinline__ Work work_at(const PackedParams& p, int64_t w) {
   Work r;
   const int64_t at = w / p.heads;
-  const PackedItem it = p.items[at];
+  const PackedItem it = p.items[item_in(p, at) ? at : 0];
   r.row0 = it.row0;
   r.len = it.len;
   r.h0 = static_cast<int>(w - at * p.heads) * p.pk;

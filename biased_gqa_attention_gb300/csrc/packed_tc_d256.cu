@@ -293,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) __cluster_dims__(2, 1, 1)
       ++no;
       ptx::tc_fence_after();
       const int64_t y0 = (static_cast<int64_t>(w.row0 + tok) * p.Hq + w.h0 + row % p.pk) * D;
-      const bool in = valid && EXTKV_IN(y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
+      const bool in = valid && EXTKV_IN_KIND(kChkOut, y0, D, static_cast<int64_t>(p.T) * p.Hq * D, p.status);
       store_row<D>(to, l, in, static_cast<__nv_bfloat16*>(p.y) + y0, [&] {
         ptx::tc_fence_before();
         ptx::mbar_arrive(&bar.o_free);

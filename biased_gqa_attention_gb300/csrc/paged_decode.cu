@@ -70,8 +70,33 @@ struct LiveKeys {
   int lo, hi;
 };
 
+__device__ __forceinline__ int64_t length_of(const PagedParams& p, int b) {
+  return EXTKV_IN_KIND(kChkLens, b, 1, p.B, p.status) ? p.nonpad[b] : 0;
+}
+
+// The pool's page that holds sequence b's slots from pg * page_size on.
+__device__ __forceinline__ int64_t page_of(const PagedParams& p, int b, int pg) {
+  const int64_t at = static_cast<int64_t>(b) * p.max_pages + pg;
+  return EXTKV_IN_KIND(kChkTable, at, 1, static_cast<int64_t>(p.B) * p.max_pages, p.status) ? p.table[at] : -1;
+}
+
+// Elements from q's, y's, the partials' start (checked builds).
+__device__ __forceinline__ bool q_in(const PagedParams& p, int64_t first) {
+  return EXTKV_IN_KIND(kChkRows, first, p.D, (p.B - 1) * p.q_stride + static_cast<int64_t>(p.Hq) * p.D, p.status);
+}
+__device__ __forceinline__ bool y_in(const PagedParams& p, int64_t first, int count) {
+  return EXTKV_IN_KIND(kChkOut, first, count, static_cast<int64_t>(p.B) * p.Hq * p.D, p.status);
+}
+__device__ __forceinline__ bool base_in(const PagedParams& p, int b) {
+  return EXTKV_IN_KIND(kChkPartial, b, 1, static_cast<int64_t>(p.B) + 1, p.status);
+}
+// rows at .. of ml and part, which have `sets` times p.rows
+__device__ __forceinline__ bool part_in(const PagedParams& p, int64_t at, int rows, int64_t sets) {
+  return EXTKV_IN_KIND(kChkPartial, at, rows, sets * p.rows, p.status);
+}
+
 __device__ __forceinline__ LiveKeys live_keys(const PagedParams& p, int b) {
-  const int64_t np = p.nonpad[b];
+  const int64_t np = length_of(p, b);
   if (np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size) return {0, 0};
   const int n = static_cast<int>(np);
   return {p.window > 0 && n > p.window ? n - p.window : 0, n};
@@ -151,12 +176,12 @@ __device__ __forceinline__ int scan_tiles(const PagedParams& p, int64_t* pre, in
   if (blockIdx.x == 0) {
     int64_t at = pre[tid];
     for (int b = b0; b < b1; ++b) {
-      p.base[b] = at;
+      if (base_in(p, b)) p.base[b] = at;
       at += tiles_of<KT>(live_keys(p, b));
-      const int64_t np = p.nonpad[b];
+      const int64_t np = length_of(p, b);
       if (np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size) report(p.status, EXTKV_DEV_BAD_NONPAD);
     }
-    if (tid == nt - 1) p.base[p.B] = pre[nt];
+    if (tid == nt - 1 && base_in(p, p.B)) p.base[p.B] = pre[nt];
   }
   return per;
 }
@@ -193,7 +218,7 @@ struct LaneScan {
   int64_t end;  // tiles (per unit) up to and with this lane's sequence
   __device__ __forceinline__ explicit LaneScan(const PagedParams& p) {
     const int lane = threadIdx.x & 31;
-    const int64_t np = lane < p.B ? p.nonpad[lane] : 0;
+    const int64_t np = lane < p.B ? length_of(p, lane) : 0;
     const bool bad = np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size;
     const int n = bad ? 0 : static_cast<int>(np);
     keys = {p.window > 0 && n > p.window ? n - p.window : 0, n};
@@ -205,8 +230,8 @@ struct LaneScan {
       if (lane >= o) end += x;
     }
     if (p.B <= 32 && blockIdx.x == 0 && threadIdx.x < 32) {
-      if (lane < p.B) p.base[lane] = end - mine;
-      if (lane == 31) p.base[p.B] = end;
+      if (lane < p.B && base_in(p, lane)) p.base[lane] = end - mine;
+      if (lane == 31 && base_in(p, p.B)) p.base[p.B] = end;
       if (bad) report(p.status, EXTKV_DEV_BAD_NONPAD);
     }
   }
@@ -245,7 +270,7 @@ struct TileRows {
       const int pg = j / p.page_size;
       off = j - pg * p.page_size;
       lead = lane == 0 || off == 0 || j == c.keys.lo;
-      page = p.table[static_cast<int64_t>(c.b) * p.max_pages + pg];
+      page = page_of(p, c.b, pg);
     }
   }
   // row of the pool in units of D elements, or ~0
@@ -256,7 +281,7 @@ struct TileRows {
       return ~0u;
     }
     const int64_t r = (page * p.Hkv + u / p.groups) * p.page_size + off;
-    if (!EXTKV_IN(r, 1, p.num_pages * p.Hkv * p.page_size, p.status)) return ~0u;
+    if (!EXTKV_IN_KIND(kChkPages, r, 1, p.num_pages * p.Hkv * p.page_size, p.status)) return ~0u;
     return static_cast<uint32_t>(r);
   }
 };
@@ -389,7 +414,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     const int unit = cta / p.cluster;
     cur.b = unit / p.units;
     cur.u = unit - cur.b * p.units;
-    const int64_t np = p.nonpad[cur.b];
+    const int64_t np = length_of(p, cur.b);
     if (tid == 0 && rank == 0 && cur.u == 0 && (np < 0 || np > static_cast<int64_t>(p.max_pages) * p.page_size))
       report(p.status, EXTKV_DEV_BAD_NONPAD);
     cur.keys = live_keys(p, cur.b);
@@ -436,7 +461,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         off[x] = j - pg * p.page_size;
         page[x] = -2;
         if (x < boxes && j < cur.keys.hi && j + p.box > cur.keys.lo)
-          page[x] = p.table[static_cast<int64_t>(cur.b) * p.max_pages + pg];
+          page[x] = page_of(p, cur.b, pg);
       }
     };
     const int groups = lane < W ? 2 * n : 0;  // K, V, K, V, ...
@@ -583,9 +608,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           const int hr = gr * kRowsU + nt * 8 + quad;  // head within the KV head's group
-          const bool in = hr < p.g;
-          const uint32_t* qr = reinterpret_cast<const uint32_t*>(
-              static_cast<const __nv_bfloat16*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + hr) * D);
+          const int64_t q_at = cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + hr) * D;
+          const bool in = hr < p.g && q_in(p, q_at);
+          const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(p.q) + q_at);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             qf[nt][kk][0] = in ? qr[kk * 8 + qi] : 0u;
@@ -748,8 +773,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             l[nt][h] += __shfl_xor_sync(0xffffffffu, l[nt][h], 16);
           }
         if (unit_end && t_first == 0) {
-          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) +
-                             (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+          const int64_t y_at = (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+          __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y_at;
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             const float i0 = l[nt][0] != 0.f ? 1.f / l[nt][0] : 0.f, i1 = l[nt][1] != 0.f ? 1.f / l[nt][1] : 0.f;
@@ -758,7 +783,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
             for (int mt = 0; mt < D / 16; ++mt) {
               const uint32_t x = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][0] * i0, o[mt][nt][1] * i1));
               const uint32_t z = ptx::movmatrix_trans(ptx::pack_bf16x2(o[mt][nt][2] * i0, o[mt][nt][3] * i1));
-              if (hr < heads) {
+              if (hr < heads && y_in(p, y_at + hr * D + mt * 16, 16)) {
                 uint32_t* yr = reinterpret_cast<uint32_t*>(y + hr * D + mt * 16);
                 yr[qi] = x;
                 yr[4 + qi] = z;
@@ -768,7 +793,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         } else if (it < n - 1) {
           // the first unit of the part, begun before it: to the workspace, the ring is still streaming
           const int64_t at = (static_cast<int64_t>(cta) * W + warp) * kRowsU;
-          leave(p.w_ml + at, p.w_part + at * D, D);
+          if (part_in(p, at, heads, static_cast<int64_t>(p.slices) * W)) leave(p.w_ml + at, p.w_part + at * D, D);
           if (lane == 0) rec[warp].early = 1;
         } else {
           // the last unit of the part: into the ring, which has been read
@@ -855,8 +880,10 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       v[W] = make_float4(0.f, 0.f, 0.f, 0.f);
       if (x.early >= 0) {
         const int64_t at = (static_cast<int64_t>(cta) * W + x.early) * kRowsU + r;
-        ml[W] = __ldcg(p.w_ml + at);
-        v[W] = __ldcg(reinterpret_cast<const float4*>(p.w_part + at * D) + c4);
+        if (part_in(p, at, 1, static_cast<int64_t>(p.slices) * W)) {
+          ml[W] = __ldcg(p.w_ml + at);
+          v[W] = __ldcg(reinterpret_cast<const float4*>(p.w_part + at * D) + c4);
+        }
       }
       float M = -INFINITY;
 #pragma unroll
@@ -875,16 +902,19 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       if (x.whole) {
         const float inv = L != 0.f ? 1.f / L : 0.f;
-        uint2* y = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) +
-                                            (static_cast<int64_t>(x.b) * p.Hq + hk * p.g + gr * kRowsU + r) * D);
-        y[c4] = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+        const int64_t y_at = (static_cast<int64_t>(x.b) * p.Hq + hk * p.g + gr * kRowsU + r) * D;
+        uint2* y = reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.y) + y_at);
+        if (y_in(p, y_at + 4 * c4, 4))
+          y[c4] = make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
       } else if constexpr (C::CLUSTER) {
         if (c4 == 0) share_ml[r] = make_float2(M, L);
         reinterpret_cast<float4*>(share + r * D)[c4] = acc;
       } else {
         const int64_t at = (static_cast<int64_t>(cta) * 2 + x.slot) * kRowsU + r;
-        if (c4 == 0) p.ml[at] = make_float2(M, L);
-        reinterpret_cast<float4*>(p.part + at * D)[c4] = acc;
+        if (part_in(p, at, 1, static_cast<int64_t>(p.slices) * 2)) {
+          if (c4 == 0) p.ml[at] = make_float2(M, L);
+          reinterpret_cast<float4*>(p.part + at * D)[c4] = acc;
+        }
       }
     }
   }
@@ -894,7 +924,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
     if (tiles_here == 0 && tid < kRowsU) share_ml[tid] = make_float2(-INFINITY, 0.f);
     __syncthreads();
     ptx::cluster_sync();
-    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + (static_cast<int64_t>(b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+    const int64_t y_at = (static_cast<int64_t>(b) * p.Hq + hk * p.g + gr * kRowsU) * D;
+    __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.y) + y_at;
     if (unit_tiles != 1 && !dead) {  // one tile: a warp has written the rows
       for (int i = rank * C::kThreads + tid; i < heads * (D / 4); i += p.cluster * C::kThreads) {
         const int r = i / (D / 4), c4 = i - r * (D / 4);
@@ -925,8 +956,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           acc.w = fmaf(wt, v[k].w, acc.w);
         }
         const float inv = L != 0.f ? 1.f / L : 0.f;  // no key: a zero row
-        reinterpret_cast<uint2*>(y + static_cast<int64_t>(r) * D)[c4] =
-            make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
+        if (y_in(p, y_at + static_cast<int64_t>(r) * D + 4 * c4, 4))
+          reinterpret_cast<uint2*>(y + static_cast<int64_t>(r) * D)[c4] =
+              make_uint2(ptx::pack_bf16x2(acc.x * inv, acc.y * inv), ptx::pack_bf16x2(acc.z * inv, acc.w * inv));
       }
     }
     __syncwarp();
@@ -1016,8 +1048,11 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
       open = true;
       t_first = cur.t;
       st.clear();
-      const T* q = static_cast<const T*>(p.q) + cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + gr * kRows) * D;
-      simt_stage_q<T, DPL>(qs, D, p.c, [&](int r) { return r < heads ? q + static_cast<int64_t>(r) * D : nullptr; });
+      const int64_t q_at = cur.b * p.q_stride + static_cast<int64_t>(hk * p.g + gr * kRows) * D;
+      const T* q = static_cast<const T*>(p.q) + q_at;
+      simt_stage_q<T, DPL>(qs, D, p.c, [&](int r) {
+        return r < heads && q_in(p, q_at + static_cast<int64_t>(r) * D) ? q + static_cast<int64_t>(r) * D : nullptr;
+      });
     }
     __syncwarp();  // tile it - 1 has been read by every lane
     if (issued < n) issue();
@@ -1048,11 +1083,12 @@ __global__ void __launch_bounds__(kSimtWarps * 32, 1) paged_decode_simt_kernel(c
     if (unit_end || it == n - 1) {
       const bool whole = unit_end && t_first == 0;
       st.reduce();
-      T* y = static_cast<T*>(p.y) + (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRows) * D;
+      const int64_t y_at = (static_cast<int64_t>(cur.b) * p.Hq + hk * p.g + gr * kRows) * D;
+      T* y = static_cast<T*>(p.y) + y_at;
       const int64_t at = (static_cast<int64_t>(slice) * 2 + slot) * kRows;
 #pragma unroll
       for (int r = 0; r < kRows; ++r) {
-        if (r < heads) {
+        if (r < heads && (whole ? y_in(p, y_at + r * D, D) : part_in(p, at + r, 1, static_cast<int64_t>(p.slices) * 2))) {
           const float inv = st.l[r] != 0.f ? 1.f / st.l[r] : 0.f;
           if (!whole && lane == 0) p.ml[at + r] = make_float2(st.m[r], st.l[r]);
 #pragma unroll
@@ -1093,8 +1129,11 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int b = blockIdx.x / p.Hq, h = blockIdx.x - b * p.Hq, D = p.D;
   const int hk = h / p.g, hr = h - hk * p.g, gr = hr / p.rows, r = hr - gr * p.rows;
+  if (!(base_in(p, b) && base_in(p, b + 1))) return;
   const int64_t b0 = p.base[b], tiles = p.base[b + 1] - b0, total = p.base[p.B] * p.units;
-  T* y = static_cast<T*>(p.y) + (static_cast<int64_t>(b) * p.Hq + h) * D;
+  const int64_t y_at = (static_cast<int64_t>(b) * p.Hq + h) * D;
+  T* y = static_cast<T*>(p.y) + y_at;
+  if (!y_in(p, y_at, D)) return;
   if (tiles == 0) {  // no key
     for (int d = tid; d < D; d += kMergeThreads) y[d] = Elem<T>::from_float(0.f);
     return;
@@ -1107,6 +1146,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
   const int n = s1 - s0 + 1;
   // partial i of the unit, in rows of the workspace
   auto at = [&](int i) { return (static_cast<int64_t>(s0 + i) * 2 + (i == 0 ? first_slot : 0)) * p.rows + r; };
+  auto there = [&](int i) { return part_in(p, at(i), 1, static_cast<int64_t>(p.slices) * 2); };
 
   // four columns of the first partials this thread adds up: on their way while
   // the weights are computed
@@ -1119,14 +1159,14 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
 #pragma unroll
     for (int u = 0; u < kAhead; ++u) {
       const int i = i0 + u * subs;
-      v[u] = sub < subs && i < n ? __ldcg(part + at(i) * cols) : make_float4(0.f, 0.f, 0.f, 0.f);
+      v[u] = sub < subs && i < n && there(i) ? __ldcg(part + at(i) * cols) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
   };
   fetch(sub);
 
   float M = -INFINITY;
   for (int i = tid; i < n; i += kMergeThreads) {
-    const float m = __ldcg(&p.ml[at(i)].x);
+    const float m = there(i) ? __ldcg(&p.ml[at(i)].x) : -INFINITY;
     w_s[i] = m;
     M = fmaxf(M, m);
   }
@@ -1141,7 +1181,7 @@ __global__ void __launch_bounds__(kMergeThreads) paged_merge_kernel(const PagedP
   for (int i = tid; i < n; i += kMergeThreads) {
     const float w = w_s[i] == -INFINITY ? 0.f : ptx::ex2(w_s[i] - ref);  // -inf: every key of the slice was skipped
     w_s[i] = w;
-    L = fmaf(w, __ldcg(&p.ml[at(i)].y), L);
+    if (there(i)) L = fmaf(w, __ldcg(&p.ml[at(i)].y), L);
   }
 #pragma unroll
   for (int o = 16; o; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);

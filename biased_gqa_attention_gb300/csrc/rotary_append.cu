@@ -51,7 +51,8 @@ struct RotaryParams {
   const int64_t* positions;
   const float* inv_freq;
   int rows_per_cta, heads_per_cta;  // heads counted over q, k, v
-  int64_t q_total, k_total;         // elements of q_out / k_out (checked builds)
+  int64_t q_total, k_total;         // elements of q_out / k_out, and of the sources (checked builds)
+  int64_t q_rows, k_rows, v_rows;
   int paged;
   const int64_t* page_table;
   const int64_t* write_idx;
@@ -166,7 +167,9 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
 #pragma unroll
     for (int a = 0; a < 3; ++a) axis += c >= p.sec_end[a] ? 1 : 0;
     axis = min(axis, p.n_axes - 1);
-    cs[r * half + (c % PV) * n_vec + c / PV] = cos_sin(p.positions[axis * p.n_rows + row0 + r], p.inv_freq[c]);
+    const int64_t pos_at = axis * p.n_rows + row0 + r;
+    if (EXTKV_IN_KIND(kChkAngles, pos_at, 1, p.n_axes * p.n_rows, p.status) && EXTKV_IN_KIND(kChkAngles, c, 1, half, p.status))
+      cs[r * half + (c % PV) * n_vec + c / PV] = cos_sin(p.positions[pos_at], p.inv_freq[c]);
   }
   if (tid >= kThreads - rows) {  // one of the last threads per row: its source and destination
     const int r = tid - (kThreads - rows);
@@ -187,12 +190,13 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
         int64_t lo = 0, hi = p.n_seqs + 1;
         while (lo < hi) {
           const int64_t mid = (lo + hi) >> 1;
+          if (!EXTKV_IN_KIND(kChkLens, mid, 1, p.n_seqs + 1, p.status)) break;
           if (p.cu[mid] <= t) lo = mid + 1;
           else hi = mid;
         }
         b = lo - 1;
         live = b >= 0 && b < p.n_seqs;
-        if (live) {
+        if (live && EXTKV_IN_KIND(kChkLens, b, 2, p.n_seqs + 1, p.status)) {
           first = p.cu[b];
           end = p.cu[b + 1];
           live = first >= 0 && first <= t && t < end && end <= p.n_rows;
@@ -203,13 +207,14 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
       pl.k_src = t * p.k.ss;
       pl.v_src = t * p.v.ss;
       pl.k_dst = pl.v_dst = -1;
-      if (live) {
+      if (live && EXTKV_IN_KIND(kChkLens, b, 1, p.n_seqs, p.status)) {
         const int64_t w = p.write_idx[b], cap = p.max_pages * p.page_size;
         if (w < 0 || w > cap - (end - first)) {
           if (t == first && blockIdx.y == 0) report(p.status, EXTKV_DEV_BAD_WRITE_IDX);
         } else {
           const int64_t slot = w + (t - first), pg = slot / p.page_size;
-          const int64_t page = p.page_table[b * p.max_pages + pg];
+          const int64_t at = b * p.max_pages + pg;
+          const int64_t page = EXTKV_IN_KIND(kChkTable, at, 1, p.n_seqs * p.max_pages, p.status) ? p.page_table[at] : -1;
           if (page < 0 || page >= p.num_pages) {
             if (blockIdx.y == 0) report(p.status, EXTKV_DEV_BAD_PAGE);
           } else {
@@ -223,6 +228,7 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
   if (p.cu && blockIdx.x == 0 && blockIdx.y == 0) {  // the whole of cu_seqlens, once
     bool bad = false;
     for (int64_t b = tid; b <= p.n_seqs; b += kThreads) {
+      if (!EXTKV_IN_KIND(kChkLens, b, 1, p.n_seqs + 1, p.status)) break;
       const int64_t x = p.cu[b];
       bad |= x < 0 || x > p.n_rows || (b > 0 && p.cu[b - 1] > x);
     }
@@ -263,9 +269,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
           const Tensor& t = is_q ? p.q : p.k;
           const int hd = is_q ? h : h - p.q.heads;
           const int64_t to = is_q ? place[r].q_dst : place[r].k_dst;
-          const int64_t d_at = to + hd * t.dh + e;
-          if (to >= 0 && EXTKV_IN(d_at, part + VW, is_q ? p.q_total : p.k_total, p.status)) {
-            src[u] = static_cast<const T*>(t.src) + (is_q ? place[r].q_src : place[r].k_src) + hd * t.sh + e;
+          const int64_t d_at = to + hd * t.dh + e, s_at = (is_q ? place[r].q_src : place[r].k_src) + hd * t.sh + e;
+          if (to >= 0 &&
+              EXTKV_IN_KIND(is_q || !p.paged ? kChkOut : kChkPages, d_at, part + VW, is_q ? p.q_total : p.k_total, p.status) &&
+              EXTKV_IN_KIND(kChkRows, s_at, part + VW, is_q ? p.q_rows : p.k_rows, p.status)) {
+            src[u] = static_cast<const T*>(t.src) + s_at;
             dst[u] = static_cast<T*>(t.dst) + d_at;
             row[u] = r;
             a[u] = *reinterpret_cast<const V*>(src[u]);
@@ -322,10 +330,11 @@ __global__ void __launch_bounds__(kThreads, kMinCtas) rotary_append_kernel(const
       dst[u] = nullptr;
       if (x < total) {
         const int r = by_nv(x), hd = hv0 + x - r * nv;
-        const int64_t d_at = place[r].v_dst + hd * p.v.dh + e;
-        if (place[r].v_dst >= 0 && EXTKV_IN(d_at, CW, p.k_total, p.status)) {
+        const int64_t d_at = place[r].v_dst + hd * p.v.dh + e, s_at = place[r].v_src + hd * p.v.sh + e;
+        if (place[r].v_dst >= 0 && EXTKV_IN_KIND(kChkPages, d_at, CW, p.k_total, p.status) &&
+            EXTKV_IN_KIND(kChkRows, s_at, CW, p.v_rows, p.status)) {
           dst[u] = static_cast<T*>(p.v.dst) + d_at;
-          a[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v.src) + place[r].v_src + hd * p.v.sh + e);
+          a[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v.src) + s_at);
         }
       }
     }
@@ -377,6 +386,13 @@ cudaError_t launch_rotary(const RotaryArgs& a) {
   }
   p.q_total = p.n_rows * a.q.heads * a.D;
   p.k_total = a.paged ? a.num_pages * a.page_size * a.k.heads * a.D : p.n_rows * a.k.heads * a.D;
+  // (sources: dense batches, or the rows of a packed tensor)
+  auto elements = [&](const RowTensor& t) {
+    return t.heads ? (a.B - 1) * t.sb + (a.S - 1) * t.ss + (t.heads - 1) * t.sh + a.D : 0;
+  };
+  p.q_rows = elements(a.q);
+  p.k_rows = elements(a.k);
+  p.v_rows = elements(a.v);
   p.paged = a.paged;
   p.page_table = a.page_table;
   p.write_idx = a.write_idx;
