@@ -1,16 +1,22 @@
 // paged_decode.cu -- attention of one new token per sequence over a cache in
 // pages.
 //
-// Bound: HBM.  Every live K and V row is read once per KV head (4 D bytes for
-// bf16), for 4 D (Hq/Hkv) flops.
+// Bound: HBM.  Every live K and V row is read once per unit: a (sequence, KV head,
+// group of query heads), 4 D bytes a key in bf16 for 4 D flops a head.  A group
+// is all heads of a KV head up to 8, or 16 (unit_rows()); a KV head with more has
+// several units, which read its rows again: two sequences of
+// 131071 and one KV head of 128, 37.8 us with 16 query heads and 85.4 with 64; of
+// 65536 and 512, 65.5 us with 8 and 92.8 with 16.
 //
-// The batch's work is one axis of tiles (KT keys of one unit; a unit is a
-// (sequence, KV head, group of query heads)), unit after unit.  Every CTA takes
-// an equal contiguous slice of it and every warp an equal part of that,
-// whatever the sequences' lengths are: a warp streams its part through its own
-// ring of shared-memory stages (16-byte cp.async, a row's address from the page
-// table, rows outside the sequence filled with zeros), so warps do not wait for
-// each other while they stream, and a page may end anywhere in a tile.  A unit
+// The batch's work is one axis of tiles (KT keys of one unit), unit after unit.
+// Every CTA takes an equal contiguous slice of it and every warp an equal part of
+// that, whatever the sequences' lengths are: a warp works through its part by
+// a ring of shared-memory slots of its own, so warps do not wait for each other
+// while they stream.  The tensor-core kernels' rings are filled by a producer warp
+// (TMA boxes of page rows; page sizes that are multiples of 16); for other page
+// sizes, and on the SIMT lanes, a warp copies its own rows (16-byte cp.async, a
+// row's address from the page table, rows outside the sequence filled with zeros),
+// and a page may end anywhere in a tile.  A unit
 // that lies in one warp's part is written out by it; a unit split over warps of
 // a CTA is joined by the CTA at its end, and one split over CTAs by the merge
 // kernel, from each CTA's (max, sum, unnormalised output) in the workspace.
@@ -1311,6 +1317,8 @@ int clusters_at_once(const void* kernel, int size, int threads, size_t smem) {
 // capacity; the axis' follows the average, plus about 4 us of joining CTAs, in
 // which an SM streams some 180 KB.  Measured (axis, cluster): 1 sequence of 517,
 // 8 KV heads of 256: 12.2, 9.7 us; 8 sequences of 8, window 1024: 22.5, 20.2 us.
+// The lengths are on the device, so without a window the bound is the table's
+// width: that one sequence in a table of 8192 slots runs on the axis (2.7 us more).
 template <class C>
 int cluster_size(const PagedParams& p, bool forced) {
   const int64_t units = static_cast<int64_t>(p.B) * p.units;

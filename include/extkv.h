@@ -335,6 +335,11 @@ int attention_ext_kv_noalloc(void *y, const void *q, const void *k_cache, const 
  *                 EXTKV_DEV_BAD_PAGE and its slots are skipped.  Sequences may
  *                 share pages that are only read.  page_size is any positive
  *                 number; num_pages * Hkv * page_size < 2^32 - 1.
+ * The attention calls on these layouts know causal and window masks; a bias,
+ * image spans and a softcap are attention_ext_kv's.  No call lets several rows
+ * of one sequence attend its pages together: the rows of a chunk behind a
+ * prefix can be attended as that many sequences that share the prefix' pages,
+ * row i with nonpad = its position + 1.
  */
 
 /*
@@ -404,17 +409,24 @@ int paged_kv_append(void *k_pages, void *v_pages, const void *k_new, const void 
  * (the token sits at position nonpad[b] - 1, its own K/V row already in the
  * pages).  q has B rows (Hq,D), q_stride elements apart; y is dense (B,Hq,D).
  * Query head h reads KV head h / (Hq/Hkv).  Statistics, products' sums and the
- * joining of split sequences are fp32; the result does not depend on timing.
+ * joining of split sequences are fp32; the tensor-core kernels round P to bf16
+ * for the P.V product (its sum is taken before that).  The result does not
+ * depend on timing.
  *   - nonpad[b] == 0 gives zero rows; nonpad outside [0, max_pages * page_size]
  *     too, flagged EXTKV_DEV_BAD_NONPAD.  Slots outside the range never reach
  *     the result, whatever they hold (NaN included); neither do those of a bad
  *     page (EXTKV_DEV_BAD_PAGE), and a row left without keys is a zero row.
- *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
- *     max_pages * page_size < 2^31.
+ *   - scale: finite and > 0; scores are formed in fp32, where
+ *     log2(e) * scale * q.K has to be finite.  Requires Hq % Hkv == 0, D % 8 == 0,
+ *     8 <= D <= 512, max_pages * page_size <= 2^31 - 256.
  *   - bf16 with D in {64,128,256,512} runs on tensor cores, every other shape
- *     on fp32 SIMT; both split the batch's keys evenly over the GPU.  Few short
- *     units (a small batch or a window, page_size a multiple of 16) run on a
- *     kernel with a cluster of CTAs per (sequence, KV head, head group) instead;
+ *     on fp32 SIMT; both split the batch's keys evenly over the GPU.  A KV head's
+ *     keys are read once for every 8 of its query heads, or 16 (tensor cores, D up
+ *     to 256, more than 8 of them).  Few short units (a small batch, page_size a
+ *     multiple of 16) run on a kernel with a cluster of CTAs per (sequence, KV
+ *     head, head group) instead.  How long a unit can be is not known on the
+ *     host: the choice goes by the window, or without one by the table's width
+ *     max_pages * page_size, so a short sequence in a wide table runs on the first;
  *     EXTKV_ALGO_DECODE_STREAMK and EXTKV_ALGO_DECODE_CLUSTER force the one or
  *     the other (EXTKV_ERR_UNSUPPORTED where the cluster kernel cannot run), and
  *     every other extkv_set_algo setting leaves the choice to the call.
@@ -439,8 +451,9 @@ size_t attention_paged_decode_workspace_size(int64_t B, int64_t Hq, int64_t Hkv,
  *   - Rows of other sequences never reach a result, whatever they hold.  A row
  *     of v that holds an infinity or a NaN may reach every row of its own
  *     sequence, as 0 * infinity does.
- *   - scale: finite and > 0.  Requires Hq % Hkv == 0, D % 8 == 0, 8 <= D <= 512,
- *     T + B <= 2^31 - 256.
+ *   - scale: finite and > 0; scores are formed in fp32, where
+ *     log2(e) * scale * q.k has to be finite.  Requires Hq % Hkv == 0, D % 8 == 0,
+ *     8 <= D <= 512, T + B <= 2^31 - 256.
  *   - bf16 with D in {64,128,256} runs on the tcgen05 tensor cores, every other
  *     shape on fp32 SIMT.  P is rounded to bf16 for the P.V product there (its
  *     sum is taken before that).
