@@ -760,18 +760,22 @@ class RecordedStep:
     """A step recorded with StepRecorder: calling it starts every recorded
     library call again with one launch, on ``stream`` (a torch stream or a raw
     handle; default the current stream).  It keeps the workspaces that its calls
-    allocated; the tensors they were given must stay alive and in place."""
+    allocated; the tensors they were given must stay alive and in place.  A step
+    launched on a raw handle is kept until its launches have finished."""
 
-    __slots__ = ("_h", "_workspaces")
+    __slots__ = ("_h", "_workspaces", "_noted")
 
     def __init__(self, handle: int, workspaces=()):
         self._h = ctypes.c_void_p(handle)
         self._workspaces = list(workspaces)
+        self._noted = set()  # streams behind whose launches freed workspaces are reused
 
     def __call__(self, stream=None):
         handle = _stream(stream)
-        for w in self._workspaces:  # freed with the step, reused only behind this launch
-            w.record_stream(torch.cuda.ExternalStream(handle or 0))
+        if self._workspaces and handle not in self._noted and not isinstance(stream, (int, torch.cuda.ExternalStream)):
+            self._noted.add(handle)
+            for w in self._workspaces:
+                w.record_stream(torch.cuda.current_stream() if stream is None else stream)
         code = load().extkv_step_launch(self._h, handle)
         if code != EXTKV_OK:
             raise ExtKVError(code, load().extkv_last_error().decode())

@@ -40,6 +40,14 @@ class FakeLibrary:
         return (lambda *a: 4096) if name.endswith(("_size", "_size_dv")) else (lambda *a: 0)
 
 
+class External:
+    def __init__(self, handle, *a):
+        self.cuda_stream = handle
+
+
+noted = []  # streams that workspaces were recorded on
+
+
 @pytest.fixture
 def fake(monkeypatch):
     lib, made = FakeLibrary(), []
@@ -56,9 +64,10 @@ def fake(monkeypatch):
     monkeypatch.setattr(ek, "_on_current_device", lambda **t: None)
     monkeypatch.setattr(torch, "empty", noted_empty)
     monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream=5))
-    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, *a: types.SimpleNamespace(cuda_stream=h))
+    monkeypatch.setattr(torch.cuda, "ExternalStream", External)
     monkeypatch.setattr(torch.cuda, "stream", lambda s: contextlib.nullcontext())
-    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: None)
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda self, s: noted.append(s.cuda_stream))
+    noted.clear()
     return made
 
 
@@ -90,7 +99,9 @@ def test_a_step_keeps_the_workspace_that_a_recorded_call_allocated(fake, name):
     del rec
     gc.collect()
     assert [w() is not None for w in fake] == [False, True, False]
-    step()
+    for stream in (None, None, types.SimpleNamespace(cuda_stream=9), 5, 11, External(12)):
+        step(stream)
+    assert noted == [5, 9]  # once a stream; a raw handle may be gone when the workspace is freed
     del step
     gc.collect()
     assert all(w() is None for w in fake)
