@@ -486,14 +486,14 @@ __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap&
   const int boxes = KT / p.box;  // per tile: 1, or 2
   int64_t page[2];
   int off[2];
-  auto look_up = [&] {  // the tile's pages; -2: not needed
+  bool needed[2];
+  auto look_up = [&] {  // the tile's pages
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       const int j = cur.key0() + x * p.box, pg = j / p.page_size;
       off[x] = j - pg * p.page_size;
-      page[x] = -2;
-      if (x < boxes && j < cur.keys.hi && j + p.box > cur.keys.lo)
-        page[x] = page_of(p, cur.b, pg);
+      needed[x] = x < boxes && j < cur.keys.hi && j + p.box > cur.keys.lo;
+      page[x] = needed[x] ? page_of(p, cur.b, pg) : -1;
     }
   };
   const int groups = lane * C::PRODUCERS + static_cast<int>(threadIdx.x >> 5) - W < W ? 2 * part.n : 0;  // K, V, K, V, ...
@@ -511,7 +511,7 @@ __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap&
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         row[x] = -1;
-        if (page[x] == -2) continue;
+        if (!needed[x]) continue;
         if (page[x] < 0 || page[x] >= p.num_pages) {
           if (cur.u == 0 && !(g & 1)) report(p.status, EXTKV_DEV_BAD_PAGE);
           continue;

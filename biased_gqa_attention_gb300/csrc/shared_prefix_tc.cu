@@ -202,10 +202,13 @@ __global__ void __maxnreg__(TcCfg<D>::kRegs)
           first_of = s.s.at.g;
           first = first_of_group(p, g);
         }
-        auto pages = [&](int kt) -> int64_t {  // of the tiles from kt on; -2: not needed
-          const int t = kt + lane / boxes, j = (g.lo / KN + t) * KN + lane % boxes * p.box;
-          return lane < ahead * boxes && t < s.t1 && j < g.hi && j + p.box > first ? prefix_page(p, s.s.at.g, j / p.page_size) : -2;
+        // the lane's box of the tiles from kt on: its first key, whether it is needed, and its page
+        auto key = [&](int kt) { return (g.lo / KN + kt + lane / boxes) * KN + lane % boxes * p.box; };
+        auto needed = [&](int kt) {
+          const int j = key(kt);
+          return lane < ahead * boxes && kt + lane / boxes < s.t1 && j < g.hi && j + p.box > first;
         };
+        auto pages = [&](int kt) -> int64_t { return needed(kt) ? prefix_page(p, s.s.at.g, key(kt) / p.page_size) : -1; };
         int64_t page = pages(s.t0), next = pages(s.t0 + ahead);
         int window = s.t0;
         uint32_t in = 0;  // whose pages lie in the pool
@@ -217,7 +220,7 @@ __global__ void __maxnreg__(TcCfg<D>::kRegs)
               next = pages(kt + ahead);
             }
             const bool good = page >= 0 && page < p.num_pages;
-            if (page != -2 && !good && s.s.at.u == 0 && !is_v) report(p.status, EXTKV_DEV_BAD_PAGE);
+            if (!good && s.s.at.u == 0 && !is_v && needed(kt)) report(p.status, EXTKV_DEV_BAD_PAGE);
             in = __ballot_sync(0xffffffffu, good);
           }
           const int k0 = (g.lo / KN + kt) * KN, at = (kt - window) * boxes;
