@@ -353,21 +353,38 @@ __device__ __forceinline__ void wait_beside() {
   if (blockIdx.x == gridDim.x - 1) ptx::grid_dependency_wait();
 }
 
-// What the warps of a CTA share besides their rings.
-template <class C>
-struct Shared {
-  int64_t pre[C::kThreads + 1], warp_sum[C::kThreads / 32];
-  uint32_t live_mask[C::WARPS][C::SLOTS];  // keys of the slot's K tile that were loaded
-  Rec rec[C::WARPS];
-  Chain chains[C::WARPS + 1];
-  int n_chains;
+// What the warps of a CTA share besides their rings: the barriers of rings that requests
+// fill, the scales of 8-bit pages, and the rest.  A kernel holds no member that it does not
+// use: at head size 512 the rings that warps copy into, 2 KB of the rest and the 1 KB that a
+// CTA costs make 196 KB, a split of the SM's memory that leaves 60 KB of L1, one byte more
+// leaves 28 (16 sequences up to 8192, 2 KV heads, pages of 7: 62 us, 65).
+template <class C, bool TMA = C::TMA>
+struct RingBars {
   uint64_t full[C::WARPS][C::SLOTS], empty[C::WARPS][C::SLOTS];
   int abort_flag;
-  // 8-bit pages: the keys' (K, V) scales of the K tiles, which lie in the even slots
-  alignas(16) uint8_t scales[C::ES == 1 ? C::WARPS : 1][C::ES == 1 ? C::SLOTS / 2 : 1][C::ES == 1 ? 2 * C::KT : 16];
-  // and of the tile at hand, for the warp's lanes: K's scale, the exponent of V's, one over V's scale
-  float4 key_scale[C::ES == 1 ? C::WARPS : 1][C::ES == 1 ? C::KT : 1];
 };
+template <class C>
+struct RingBars<C, false> {};
+template <class C, bool CODES = C::ES == 1>
+struct CodeScales {
+  alignas(16) uint8_t scales[C::WARPS][C::SLOTS / 2][2 * C::KT];  // the keys' (K, V) scales of the K tiles, which lie in the even slots
+  // and of the tile at hand, for the warp's lanes: K's scale, the exponent of V's, one over V's scale
+  float4 key_scale[C::WARPS][C::KT];
+};
+template <class C>
+struct CodeScales<C, false> {};
+template <class C>
+struct Shared : RingBars<C>, CodeScales<C> {
+  int64_t pre[C::kThreads + 1], warp_sum[C::kThreads / 32];
+  Chain chains[C::WARPS + 1];
+  int n_chains;
+};
+// Keys of each slot's K tile that were loaded, and the warps' records: arrays of their own, since as
+// members of Shared they cost the copying kernels registers (66 us above).
+template <class C>
+using LiveMasks = uint32_t[C::WARPS][C::SLOTS];
+template <class C>
+using Recs = Rec[C::WARPS];
 
 // Bounded wait: polls first (the warp has its scheduler almost to itself), then
 // suspends; gives up once another warp has.
@@ -395,7 +412,7 @@ template <class C>
 __device__ __forceinline__ void init_rings(const CUtensorMap& kmap, const CUtensorMap& vmap, Shared<C>& sh) {
   constexpr int W = C::WARPS, NS = C::SLOTS;
   const int tid = threadIdx.x;
-  if (C::TMA) {
+  if constexpr (C::TMA) {
     for (int i = tid; i < W * NS; i += C::kThreads) {
       ptx::mbar_init(&sh.full[i / NS][i % NS], C::ES == 1 && i % NS % 2 == 0 ? 2 : 1);  // (a K tile's scales)
       ptx::mbar_init(&sh.empty[i / NS][i % NS], 1);
@@ -475,7 +492,7 @@ __device__ __forceinline__ bool start_part(const PagedParams& p, int64_t* pre, i
 // brings its keys' scales along.
 template <class C>
 __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
-                                        Shared<C>& sh, const Part<C>& part) {
+                                        Shared<C>& sh, LiveMasks<C>& live_mask, const Part<C>& part) {
   constexpr int D = C::D, KT = C::KT, NS = C::SLOTS, W = C::WARPS;
   // a row is chunks of 128 bytes, or half of one (64 bytes: two keys share a 128-byte row)
   constexpr int kPerKey = D * C::ES < 128 ? D * C::ES : 128, kChunks = D * C::ES / kPerKey;
@@ -520,7 +537,7 @@ __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap&
         bytes += p.box * D * C::ES;
         mask |= (p.box == 32 ? ~0u : (1u << p.box) - 1u) << (x * p.box);
       }
-      sh.live_mask[part.mine][slot] = mask;
+      live_mask[part.mine][slot] = mask;
       if (bytes) {
         ptx::mbar_arrive_expect_tx(&sh.full[part.mine][slot], bytes);
 #pragma unroll
@@ -583,15 +600,15 @@ __device__ __forceinline__ void store4(float* y, float4 a, float inv) {
 
 // The end of every consumer and producer: units split over this CTA's warps (and maybe its neighbours).
 template <class C, typename T>
-__device__ __forceinline__ void join_parts(const PagedParams& p, uint8_t* smem, Shared<C>& sh, const Part<C>& part) {
+__device__ __forceinline__ void join_parts(const PagedParams& p, uint8_t* smem, Shared<C>& sh, const Recs<C>& rec, const Part<C>& part) {
   constexpr int D = C::D, NT = C::NT, W = C::WARPS;
   constexpr int kRowsU = 8 * NT, kPad = D + 4;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, cta = blockIdx.x;
   const int tiles_here = part.tiles_here, unit_tiles = part.unit_tiles, rank = part.rank;
-  volatile int* abort = &sh.abort_flag;
   // ---- the units split over this CTA's warps (and maybe its neighbours)
   __syncthreads();
-  const bool dead = C::TMA && *abort;  // nothing to join: a part is missing
+  bool dead = false;  // nothing to join: a part is missing
+  if constexpr (C::TMA) dead = *static_cast<volatile int*>(&sh.abort_flag);
   if (dead && tid == 0) report(p.status, EXTKV_DEV_TIMEOUT);
   if (!C::CLUSTER && dead) return;
   float* share = reinterpret_cast<float*>(smem + W * C::kRing);  // cluster: this CTA's rows, then their (max, sum)
@@ -600,7 +617,7 @@ __device__ __forceinline__ void join_parts(const PagedParams& p, uint8_t* smem, 
     // lane k looks at warp k's part; a unit's warps are neighbours, so the
     // members of a chain are the late partials of its unit and the early one
     // that ends it, if there is one
-    const Rec r = sh.rec[min(lane, W - 1)];
+    const Rec r = rec[min(lane, W - 1)];
     const bool some = lane < W && r.n > 0;
     const unsigned busy = __ballot_sync(0xffffffffu, some);
     const int64_t head = static_cast<int64_t>(r.b[0]) * p.units + r.u[0];
@@ -753,7 +770,8 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared<C> sh;
-  volatile int* abort = &sh.abort_flag;
+  __shared__ LiveMasks<C> live_mask;
+  __shared__ Recs<C> rec;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quad = lane >> 2, qi = lane & 3;
   init_rings<C>(kmap, vmap, sh);
@@ -767,10 +785,13 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
   const int cta = blockIdx.x, n = part.n;
   Cursor<KT> cur = part.cur;
 
-  if (C::TMA && warp >= W) {
-    produce<C>(p, kmap, vmap, smem, sh, part);
-  } else {
-    if (lane == 0) sh.rec[warp] = Rec{};
+  bool producer = false;
+  if constexpr (C::TMA) {
+    producer = warp >= W;
+    if (producer) produce<C>(p, kmap, vmap, smem, sh, live_mask, part);
+  }
+  if (!producer) {
+    if (lane == 0) rec[warp] = Rec{};
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
     // place of 16-byte piece ch of row r in a slot
     auto piece = [](int r, int ch) { return static_cast<uint32_t>((ch >> 3) * (KT * 128) + r * 128 + (((ch & 7) ^ (r & 7)) << 4)); };
@@ -787,7 +808,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
       if (!is_v) {
         row = rows.row(p);
         const uint32_t mask = __ballot_sync(0xffffffffu, row != ~0u);
-        if (lane == 0) sh.live_mask[warp][s] = mask;
+        if (lane == 0) live_mask[warp][s] = mask;
       }
       const uint8_t* src = static_cast<const uint8_t*>(is_v ? p.v : p.k);
       constexpr int kChunks = D / 8;  // 16-byte pieces of a row
@@ -842,9 +863,9 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
         open = true;
         t_first = cur.t;
         if (it == 0 && lane == 0) {
-          sh.rec[warp].n = n;
-          sh.rec[warp].b[0] = cur.b;
-          sh.rec[warp].u[0] = cur.u;
+          rec[warp].n = n;
+          rec[warp].b[0] = cur.b;
+          rec[warp].u[0] = cur.u;
         }
         const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
 #pragma unroll
@@ -870,12 +891,12 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
       }
       // K has landed
       if constexpr (C::TMA) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, abort, p.wait_limit))) break;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, &sh.abort_flag, p.wait_limit))) break;
       } else {
         cp_async_wait<NS - 2>();
         __syncwarp();  // for every lane, and V of the tile before has been read by every lane
       }
-      const uint32_t mask = sh.live_mask[warp][sk] & key_bits<KT>(cur.keys.lo, cur.keys.hi, cur.key0());
+      const uint32_t mask = live_mask[warp][sk] & key_bits<KT>(cur.keys.lo, cur.keys.hi, cur.key0());
       if constexpr (!C::TMA) {
         issue();
         cp_async_commit();
@@ -964,7 +985,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
       }
       // V has landed
       if constexpr (C::TMA) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, abort, p.wait_limit))) break;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, &sh.abort_flag, p.wait_limit))) break;
         if (mask != kFull) {
           // rows of masked keys, whatever they hold, become zeros: their P is 0, and 0 * NaN would be NaN
           uint8_t* vt = smem + warp * C::kRing + sk * C::kTile;
@@ -1039,7 +1060,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
           // the first unit of the part, begun before it: to the workspace, the ring is still streaming
           const int64_t at = (static_cast<int64_t>(cta) * W + warp) * kRowsU;
           if (part_in(p, at, heads, static_cast<int64_t>(p.slices) * W)) leave(p.w_ml + at, p.w_part + at * D, D);
-          if (lane == 0) sh.rec[warp].early = 1;
+          if (lane == 0) rec[warp].early = 1;
         } else {
           // the last unit of the part: into the ring, which has been read
           if (!C::TMA) cp_async_wait<0>();
@@ -1047,11 +1068,11 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
           float* dst = reinterpret_cast<float*>(smem + warp * C::kRing);
           leave(reinterpret_cast<float2*>(dst + kRowsU * kPad), dst, kPad);
           if (lane == 0) {
-            sh.rec[warp].late = 1;
-            sh.rec[warp].begins = t_first == 0;
-            sh.rec[warp].ends = unit_end;
-            sh.rec[warp].b[1] = cur.b;
-            sh.rec[warp].u[1] = cur.u;
+            rec[warp].late = 1;
+            rec[warp].begins = t_first == 0;
+            rec[warp].ends = unit_end;
+            rec[warp].b[1] = cur.b;
+            rec[warp].u[1] = cur.u;
           }
         }
         open = false;
@@ -1059,7 +1080,7 @@ __global__ void __launch_bounds__(C::kThreads, C::CTAS)
       cur.next(p);
     }
   }
-  join_parts<C, __nv_bfloat16>(p, smem, sh, part);
+  join_parts<C, __nv_bfloat16>(p, smem, sh, rec, part);
   if (C::PARTIAL) wait_beside();
 }
 

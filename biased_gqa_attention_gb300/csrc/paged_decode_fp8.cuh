@@ -25,7 +25,8 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   __shared__ Shared<C> sh;
-  volatile int* abort = &sh.abort_flag;
+  __shared__ LiveMasks<C> live_mask;
+  __shared__ Recs<C> rec;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int quad = lane >> 2, qi = lane & 3;
   init_rings<C>(kmap, vmap, sh);
@@ -36,10 +37,13 @@ __global__ void __launch_bounds__(C::kThreads, 1)
   const int cta = blockIdx.x, n = part.n;
   Cursor<KT> cur = part.cur;
 
-  if (C::TMA && warp >= W) {
-    produce<C>(p, kmap, vmap, smem, sh, part);
-  } else {
-    if (lane == 0) sh.rec[warp] = Rec{};
+  bool producer = false;
+  if constexpr (C::TMA) {
+    producer = warp >= W;
+    if (producer) produce<C>(p, kmap, vmap, smem, sh, live_mask, part);
+  }
+  if (!producer) {
+    if (lane == 0) rec[warp] = Rec{};
     const uint32_t ring = ptx::smem_u32(smem) + warp * C::kRing;
     constexpr int kPieces = D / 16;  // 16-byte pieces of a row
     // place of piece ch of row r in a slot; rows of 64 bytes lie in pairs
@@ -61,7 +65,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       if (!is_v) {
         row = rows.row(p);
         const uint32_t mask = __ballot_sync(0xffffffffu, row != ~0u);
-        if (lane == 0) sh.live_mask[warp][s] = mask;
+        if (lane == 0) live_mask[warp][s] = mask;
         if (row != ~0u) scale = reinterpret_cast<const uint16_t*>(p.scales)[row];
       } else if (lane < KT) {
         reinterpret_cast<uint16_t*>(sh.scales[warp][s / 2])[lane] = static_cast<uint16_t>(scale);
@@ -118,9 +122,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
         open = true;
         t_first = cur.t;
         if (it == 0 && lane == 0) {
-          sh.rec[warp].n = n;
-          sh.rec[warp].b[0] = cur.b;
-          sh.rec[warp].u[0] = cur.u;
+          rec[warp].n = n;
+          rec[warp].b[0] = cur.b;
+          rec[warp].u[0] = cur.u;
         }
         const int hk = cur.u / p.groups, gr = cur.u - hk * p.groups;
 #pragma unroll
@@ -179,12 +183,12 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       // K has landed
       if constexpr (C::TMA) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, abort, p.wait_limit))) break;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, &sh.abort_flag, p.wait_limit))) break;
       } else {
         cp_async_wait<NS - 2>();
         __syncwarp();  // for every lane, and V of the tile before has been read by every lane
       }
-      const uint32_t mask = sh.live_mask[warp][sk] & key_bits<KT>(cur.keys.lo, cur.keys.hi, cur.key0());
+      const uint32_t mask = live_mask[warp][sk] & key_bits<KT>(cur.keys.lo, cur.keys.hi, cur.key0());
       if (lane < KT) {  // a key's scales are taken apart once
         const uint32_t both = reinterpret_cast<const uint16_t*>(sh.scales[warp][sk / 2])[lane];
         const int kb = fp8::clamp_byte(both & 0xff), vb = fp8::clamp_byte(both >> 8);
@@ -323,7 +327,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       }
       // V has landed
       if constexpr (C::TMA) {
-        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, abort, p.wait_limit))) break;
+        if (!__all_sync(0xffffffffu, wait_or_abort(&sh.full[warp][sk], pk, &sh.abort_flag, p.wait_limit))) break;
         if (mask != kFull) {
           // rows of masked keys, whatever they hold, become zeros: their P is 0, and 0 * NaN would be NaN
           uint8_t* vt = smem + warp * C::kRing + sk * C::kTile;
@@ -406,7 +410,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           // the first unit of the part, begun before it: to the workspace, the ring is still streaming
           const int64_t at = (static_cast<int64_t>(cta) * W + warp) * kRowsU;
           if (part_in(p, at, heads, static_cast<int64_t>(p.slices) * W)) leave(p.w_ml + at, p.w_part + at * D, D);
-          if (lane == 0) sh.rec[warp].early = 1;
+          if (lane == 0) rec[warp].early = 1;
         } else {
           // the last unit of the part: into the ring, which has been read
           if (!C::TMA) cp_async_wait<0>();
@@ -414,11 +418,11 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           float* dst = reinterpret_cast<float*>(smem + warp * C::kRing);
           leave(reinterpret_cast<float2*>(dst + kRowsU * kPad), dst, kPad);
           if (lane == 0) {
-            sh.rec[warp].late = 1;
-            sh.rec[warp].begins = t_first == 0;
-            sh.rec[warp].ends = unit_end;
-            sh.rec[warp].b[1] = cur.b;
-            sh.rec[warp].u[1] = cur.u;
+            rec[warp].late = 1;
+            rec[warp].begins = t_first == 0;
+            rec[warp].ends = unit_end;
+            rec[warp].b[1] = cur.b;
+            rec[warp].u[1] = cur.u;
           }
         }
         open = false;
@@ -426,7 +430,7 @@ __global__ void __launch_bounds__(C::kThreads, 1)
       cur.next(p);
     }
   }
-  join_parts<C, TQ>(p, smem, sh, part);
+  join_parts<C, TQ>(p, smem, sh, rec, part);
 }
 
 // Tiles of KT keys, SLOTS slots, WARPS consumers.
