@@ -494,8 +494,8 @@ template <class C>
 __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap& kmap, const CUtensorMap& vmap, uint8_t* smem,
                                         Shared<C>& sh, LiveMasks<C>& live_mask, const Part<C>& part) {
   constexpr int D = C::D, KT = C::KT, NS = C::SLOTS, W = C::WARPS;
-  // a row is chunks of 128 bytes, or half of one (64 bytes: two keys share a 128-byte row)
-  constexpr int kPerKey = D * C::ES < 128 ? D * C::ES : 128, kChunks = D * C::ES / kPerKey;
+  constexpr int kChunks = D * C::ES / 128;  // of a row: 128 bytes each
+  static_assert(D * C::ES % 128 == 0, "rows of whole chunks");
   const int lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort_flag;
   Cursor<KT> cur = part.cur;
@@ -543,14 +543,13 @@ __device__ __forceinline__ void produce(const PagedParams& p, const CUtensorMap&
 #pragma unroll
         for (int x = 0; x < 2; ++x)
           if (row[x] >= 0) {
-            const int at = off[x] * kPerKey / 128;
             // chunk by chunk where the box is half a tile: a box lands its chunks one after another
             if (p.box == KT) {
-              ptx::tma_load_4d(dst, map, &sh.full[part.mine][slot], 0, at, row[x], 0);
+              ptx::tma_load_4d(dst, map, &sh.full[part.mine][slot], 0, off[x], row[x], 0);
             } else {
 #pragma unroll 1
               for (int ch = 0; ch < kChunks; ++ch)
-                ptx::tma_load_4d(dst + ch * (KT * kPerKey) + x * (p.box * kPerKey), map, &sh.full[part.mine][slot], 0, at, row[x], ch);
+                ptx::tma_load_4d(dst + ch * (KT * 128) + x * (p.box * 128), map, &sh.full[part.mine][slot], 0, off[x], row[x], ch);
             }
             if constexpr (C::ES == 1) {
               if (!(g & 1)) {
@@ -1553,13 +1552,12 @@ cudaError_t launch_rings(RingKernel k, PagedParams p, cudaStream_t s) {
   std::memset(&kmap, 0, sizeof kmap);
   std::memset(&vmap, 0, sizeof vmap);
   if (C::TMA) {
-    // (128 bytes as 64 columns, row of a page, page and head, 128-byte chunk of a row);
-    // rows of 64 bytes in pairs, which lie one after another
+    // (128 bytes as 64 columns, row of a page, page and head, 128-byte chunk of a row)
     p.box = p.page_size % C::KT == 0 ? C::KT : 16;
-    constexpr uint32_t kRowBytes = C::D * C::ES, kPair = kRowBytes < 128 ? 128 / kRowBytes : 1, kChunks = kRowBytes * kPair / 128;
-    const uint64_t dims[4] = {64, static_cast<uint64_t>(p.page_size) / kPair, static_cast<uint64_t>(p.num_pages) * p.Hkv, kChunks};
-    const uint64_t str[3] = {kRowBytes * kPair, static_cast<uint64_t>(p.page_size) * kRowBytes, 128};
-    const uint32_t box[4] = {64, static_cast<uint32_t>(p.box) / kPair, 1, p.box == C::KT ? kChunks : 1u};
+    constexpr uint32_t kRowBytes = C::D * C::ES, kChunks = kRowBytes / 128;
+    const uint64_t dims[4] = {64, static_cast<uint64_t>(p.page_size), static_cast<uint64_t>(p.num_pages) * p.Hkv, kChunks};
+    const uint64_t str[3] = {kRowBytes, static_cast<uint64_t>(p.page_size) * kRowBytes, 128};
+    const uint32_t box[4] = {64, static_cast<uint32_t>(p.box), 1, p.box == C::KT ? kChunks : 1u};
     if (!make_tensor_map_bf16(&kmap, p.k, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B) ||
         !make_tensor_map_bf16(&vmap, p.v, 4, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))
       return cudaErrorInvalidValue;
