@@ -182,6 +182,7 @@ __global__ void __maxnreg__(TcCfg<D>::kRegs)
       return few ? scan.cursor(p, axis, f) : prefix_cursor<KN, kFinders>(p, pre, per, axis, mean, f);
     });
     if (tid == 0) bar.slice = slice;
+    if (!few) ptx::fence_proxy_async_smem();  // the sums' stores before Q's requests to the same place
     meet<2, C::kThreads>();  // the rows' warps have it; the sums have been read
     if (warp == 0 || warp == 3) {
       // ---------------- loads: K, and V by a warp of its own ----------------
