@@ -530,6 +530,7 @@ cudaError_t launch_shared_prefix(const SharedPrefixArgs& a, const char** name) {
   f.status = d.status;
   const bool f32 = d.dtype == EXTKV_F32;
   *name = tc ? "shared_prefix_tcgen05" : f32 ? "shared_prefix_simt_f32" : "shared_prefix_simt_bf16";
+  if (!beside && can_run_beside(p.g, d.D, tc)) *name = "shared_prefix_tcgen05_after";
   cudaError_t e = tc    ? launch_prefix_tc(f, d.stream)
                   : f32 ? launch_simt_prefix_d<float>(f, d.stream)
                         : launch_simt_prefix_d<__nv_bfloat16>(f, d.stream);

@@ -549,7 +549,8 @@ size_t attention_paged_decode_fp8_workspace_size(int64_t B, int64_t Hq, int64_t 
  *     8 <= D <= 512.  bf16 with D in {64,128,256} and page_size a multiple of 16 attends the
  *     prefix on the tcgen05 tensor cores, every other shape on fp32 SIMT; the
  *     own slots as attention_paged_decode does on its axis of tiles (extkv_set_algo
- *     does not matter here).
+ *     does not matter here).  At D = 128 with up to 8 query heads a KV head the own slots can
+ *     be attended beside the prefix; extkv_last_kernel() ends in "_after" where they come after it.
  * workspace: attention_shared_prefix_decode_workspace_size(...) bytes, 256-byte aligned,
  * as for attention_ext_kv (calls that can overlap need their own).
  */
