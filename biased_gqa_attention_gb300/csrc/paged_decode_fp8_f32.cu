@@ -1,5 +1,6 @@
 // paged_decode_fp8_f32.cu -- the decode over 8-bit pages for fp32 q and y: q and the
-// weights as two fp16 parts each, so that every product is exact and the result fp32's.
+// weights as two fp16 parts each.  A part times a code is exact and summed in fp32; the parts hold
+// q to 2^-23 of its row's largest element, and a weight to 2^-22 of it or 2^-35 of the largest.
 #include "paged_decode_fp8.cuh"
 
 namespace extkv {

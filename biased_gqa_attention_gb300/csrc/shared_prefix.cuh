@@ -100,10 +100,15 @@ __device__ __forceinline__ bool whole_in(const PrefixParams& p, int64_t row) {
 // start or end of its unit is moved there, which saves a part.
 //
 // There are as many slices as SMs (or warps) where rows are few.  Where they fill units each
-// slice leaves as many partial rows, which the join reads: n slices then cost total / n
-// tiles and, in the end, about n / 4, least at n = 2 sqrt(total).  The SMs left over take the own
-// pages.  64 sequences of 4 heads a KV head behind 8191 keys (1024 tiles): 60 us with 152
-// slices, 55 with 85, 53 with 64, 66 with 43.
+// slice leaves as many partial rows, which it writes and the join reads: n slices then cost total / n
+// tiles and, in the end, about n / 4, least at n = 2 sqrt(total).  Own pages beside the prefix get
+// the SMs left over.  64 sequences of 4 heads a KV head behind 8191 keys (1024 tiles): 60 us with 152
+// slices, 55 with 85, 53 with 64, 66 with 43.  So many at most, and as many as SMs (us a call behind a
+// flush of L2): 64 sequences of 32 heads, 8 KV heads, behind 8191, own slots up to 100 / 1000, head size 128 48
+// and 63 / 73 and 74, 64 43 and 54 / 71 and 70, 256 (16 heads, 4 KV heads) 46 and 62 / 86 and 89; 32 of 32 heads, 2
+// KV heads of 128, behind 16384 48 and 58 / 49 and 63; 64 of 4 heads, one KV head, behind 131072 58 and
+// 68 (head size 64, behind 65536, 43 and 52); 32 of them, head size 256, behind 65536 48 and 60; 32 of 32 heads,
+// 8 KV heads, behind 8191 (128 rows) 42 and 48; four groups of 64 behind 2000 75 and 75.
 constexpr int kCost = 6;
 struct SliceAxis {
   int64_t total;

@@ -22,7 +22,8 @@
 // Registers (112 a thread at launch, from which the rows' warps take 128 and leave the
 // others 72) and a ring of two K and two V tiles leave room on the SM for a CTA of the
 // own pages' kernel (shared_prefix.cu), which runs beside this one.  64 sequences of 32 heads
-// of 128 behind 8191 keys: 53 us the call, 74 where the kernels follow one another.
+// of 128 behind 8191 keys: 53 us the call, 74 where the kernels follow one another.  (Head size 64 has the
+// same shares, although own pages follow it: with more registers a thread it was not measured.)
 // Measured otherwise: tiles of 128 keys, with P over the S it is made from (both fill tensor
 // memory), take 6000 clocks where two tiles of 64 take 3800, since each waits for the
 // product before; one warp that issues everything 5000 (a product issued by a lane that the

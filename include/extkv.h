@@ -513,8 +513,18 @@ int paged_kv_read_fp8(void *k_out, void *v_out, const void *k_pages, const void 
 
 /*
  * attention_paged_decode over 8-bit pages: K[j] and V[j] are the values that the codes
- * and scales stand for; q and y are of `dtype`.  Everything else as attention_paged_decode
- * (window, lengths, flags, zero rows, garbage outside the range, workspace rules).
+ * and scales stand for; q and y are of `dtype`.  Window, lengths, flags, zero rows, garbage
+ * outside the range, sums and joins in fp32, the choice between the two forms of the tensor-core
+ * kernels and the workspace rules as attention_paged_decode.  Different from it:
+ *   - bf16 with D in {64,128,256,512} and fp32 with D in {64,128,256} run on tensor cores, in
+ *     fp16, which holds every code exactly; other shapes on fp32 SIMT.  A row of q is brought into
+ *     fp16's range by a power of two: a bf16 element is off by at most 2^-39 of the row's largest, an fp32
+ *     one (two fp16 parts) by 2^-23 of it.
+ *   - There the weights p_j 2^e_j (e_j: the exponent of V's scale) are rounded to fp16, by at most
+ *     2^-11 of each, or 2^-31 of the row's largest where that is more; for fp32 to two fp16 parts, by
+ *     2^-22 of each or 2^-35 of the largest.
+ *   - A KV head's keys are read once for every 8 of its query heads, or 16 where it has more (bf16
+ *     with D up to 256, fp32 up to 128).
  */
 int attention_paged_decode_fp8(void *y, const void *q, const void *k_pages, const void *v_pages,
                                const uint8_t *kv_scales, const int64_t *page_table, const int64_t *nonpad, float scale,
@@ -534,9 +544,9 @@ size_t attention_paged_decode_fp8_workspace_size(int64_t B, int64_t Hq, int64_t 
  *     y[b,h] = softmax_j(scale * q[b,h] . K[j]) V[j],  j over prefix, then own slots;
  * with window > 0 over the last `window` of them all.  The result is that of
  * attention_paged_decode on a table that holds the prefix' pages in front of each
- * sequence's own (were prefix_len whole pages), but a prefix' keys are read once for all rows of its
- * group: 256 rows (128 at D = 256; a row is a sequence and a query head of the KV head)
- * at a time.  Both tables name pages of the one pool (num_pages).
+ * sequence's own (were prefix_len whole pages), but a prefix' keys are read once for many rows of its
+ * group (a row is a sequence and a query head of the KV head): on the tensor cores for 256 at a time, 128
+ * at D = 256, elsewhere for 8.  Both tables name pages of the one pool (num_pages).
  *   - nonpad outside [0, max_pages * page_size] and prefix_len outside
  *     [0, max_prefix_pages * page_size] are flagged EXTKV_DEV_BAD_NONPAD; the sequence's
  *     row, or those of the group's sequences, are zero rows.  A cu_groups that breaks its rules is flagged
@@ -551,6 +561,11 @@ size_t attention_paged_decode_fp8_workspace_size(int64_t B, int64_t Hq, int64_t 
  *     own slots as attention_paged_decode does on its axis of tiles (extkv_set_algo
  *     does not matter here).  At D = 128 with up to 8 query heads a KV head the own slots can
  *     be attended beside the prefix; extkv_last_kernel() ends in "_after" where they come after it.
+ *   - Where it pays (GB300): a call has a start, a prefix of its own pass and a join, about 20 us.  8
+ *     sequences of 32 heads behind 8192 slots (8 KV heads of 128) take 30 us, and 44 by
+ *     attention_paged_decode on such tables, 64 of them 42 and 260; 4 of them 26 and 25, 4 behind 1024 19
+ *     and 10.  bf16 off the tensor cores is slower than that call: 16 sequences behind 8192, 2 KV heads
+ *     of 512, 1049 and 53 us; behind 4096, 8 KV heads of 128, pages of 7 slots, 152 and 45.
  * workspace: attention_shared_prefix_decode_workspace_size(...) bytes, 256-byte aligned,
  * as for attention_ext_kv (calls that can overlap need their own).
  */
