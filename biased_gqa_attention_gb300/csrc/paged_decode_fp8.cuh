@@ -154,8 +154,9 @@ __global__ void __launch_bounds__(C::kThreads, 1)
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
           top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
           // times a power of two that puts the largest in [2^14, 2^15): a bf16 element
-          // is exact in fp16 then, or off by 2^-39 of the largest
-          const int e = max((__float_as_int(top) >> 23) - 127, -100);
+          // is exact in fp16 then, or off by 2^-39 of the largest.  (Below 2^-112 times 2^126, the most that
+          // leaves its inverse a normal number: the least fp32 becomes 2^-23, which fp16 holds.)
+          const int e = max((__float_as_int(top) >> 23) - 127, -112);
           const float up = __int_as_float((127 + 14 - e) << 23);
           const float down = p.c * __int_as_float((127 - 14 + e) << 23);
 #pragma unroll
