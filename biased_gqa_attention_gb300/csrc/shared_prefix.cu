@@ -213,6 +213,127 @@ struct JoinParams {
   int pre_tile;  // keys of a tile of the prefixes' axis
 };
 
+// A partial: its (max, sum) and its row.
+struct Place {
+  const float2* ml;
+  const float* rows;
+};
+
+// Where the partials of a row's own slots lie: a whole unit's, or one of each of n slices from s on.
+struct OwnParts {
+  int n, s, slot, r;
+  __device__ __forceinline__ OwnParts(const PagedParams& p, int64_t own0, int64_t own1, int64_t total, int hk, int hr)
+      : n(0), s(0), slot(0), r(hr % p.rows) {
+    if (const int64_t tiles = own1 - own0; tiles > 0) {
+      const Axis axis(p, total);
+      const int64_t u0 = own0 * p.units + static_cast<int64_t>(hk * p.groups + hr / p.rows) * tiles;
+      s = axis.holds(u0);
+      n = axis.holds(u0 + tiles - 1) - s + 1;
+      slot = axis.start(s) < u0 ? 1 : 0;
+    }
+  }
+  __device__ __forceinline__ Place at(const PagedParams& p, int64_t row, int i) const {
+    if (n == 1) return own_in(p, row, 1) ? Place{p.own_ml + row, p.own_part + row * p.D} : Place{nullptr, nullptr};
+    const int64_t x = (static_cast<int64_t>(s + i) * 2 + (i == 0 ? slot : 0)) * p.rows + r;
+    return part_in(p, x, 1, static_cast<int64_t>(p.slices) * 2) ? Place{p.ml + x, p.part + x * p.D} : Place{nullptr, nullptr};
+  }
+};
+
+// Four elements of a row as fp32.
+__device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
+__device__ __forceinline__ float4 load4(const __nv_bfloat16* p) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xffff0000u), __uint_as_float(w.y << 16),
+                     __uint_as_float(w.y & 0xffff0000u));
+}
+
+// A row and its result by one warp, from keys [lo, hi) of group g's prefix and its own slots' partials.  The
+// prefix' kernels multiply a row of V by the weights of all rows of a unit, by 0 for those that do not attend
+// it, which an infinity or a NaN turns into NaN: rows that this can have reached are attended again here,
+// with their own keys alone.  Slow, since a warp takes key after key, and only for such rows: 64 sequences of 32
+// heads, windows of 4096 behind 8192, an infinity that some of them attend: 1.3 ms, 61 us with finite pages.
+template <typename T, int VPL>
+__device__ __noinline__ void attend_alone(const JoinParams& jp, int g, int b, int h, int lo, int hi, OwnParts own) {
+  const PagedParams& p = jp.own;
+  const PrefixParams& f = jp.pre;
+  constexpr int kAhead = VPL == 1 ? 4 : 2;
+  const int lane = threadIdx.x & 31, D = f.D, hk = h / f.g;
+  const int64_t y_row = static_cast<int64_t>(b) * f.Hq + h;
+  const int64_t q_at = b * f.q_stride + static_cast<int64_t>(h) * D;
+  const bool q_in = EXTKV_IN_KIND(kChkRows, q_at, D, (f.B - 1) * f.q_stride + static_cast<int64_t>(f.Hq) * D, f.status);
+  float M = -INFINITY, L = 0.f;
+  float4 q[VPL], a[VPL];
+  int at[VPL];  // the lane's columns; -1: none
+#pragma unroll
+  for (int v = 0; v < VPL; ++v) {
+    at[v] = lane + 32 * v < D / 4 ? 4 * (lane + 32 * v) : -1;
+    q[v] = at[v] >= 0 && q_in ? load4(static_cast<const T*>(f.q) + q_at + at[v]) : make_float4(0.f, 0.f, 0.f, 0.f);
+    q[v] = make_float4(q[v].x * f.c, q[v].y * f.c, q[v].z * f.c, q[v].w * f.c);
+    a[v] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+  // (max m, sum l, columns x) joined to the row's
+  auto add = [&](float m, float l, const float4 (&x)[VPL]) {
+    const float mn = fmaxf(M, m), ref = mn == -INFINITY ? 0.f : mn;
+    const float old = M == -INFINITY ? 0.f : ptx::ex2(M - ref), w = m == -INFINITY ? 0.f : ptx::ex2(m - ref);
+    M = mn;
+    L = fmaf(w, l, L * old);
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      a[v] = make_float4(fmaf(w, x[v].x, a[v].x * old), fmaf(w, x[v].y, a[v].y * old), fmaf(w, x[v].z, a[v].z * old),
+                         fmaf(w, x[v].w, a[v].w * old));
+  };
+  for (int j0 = lo; j0 < hi; j0 += 32) {
+    const int n = min(32, hi - j0);
+    int64_t row = -1;
+    if (lane < n) {
+      const int pg = (j0 + lane) / f.page_size, off = j0 + lane - pg * f.page_size;
+      const int64_t page = prefix_page(f, g, pg);
+      if (page >= 0 && page < f.num_pages) row = (page * f.Hkv + hk) * f.page_size + off;
+      if (row >= 0 && !EXTKV_IN_KIND(kChkPages, row, 1, f.num_pages * f.Hkv * f.page_size, f.status)) row = -1;
+    }
+    for (int i0 = 0; i0 < n; i0 += kAhead) {
+      int64_t pr[kAhead];
+      float4 k[kAhead][VPL], x[kAhead][VPL];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        pr[i] = __shfl_sync(0xffffffffu, row, i0 + i);  // 32 % kAhead == 0; -1 behind the last key
+#pragma unroll
+        for (int v = 0; v < VPL; ++v) {
+          const bool in = pr[i] >= 0 && at[v] >= 0;
+          k[i][v] = in ? load4(static_cast<const T*>(f.k) + pr[i] * D + at[v]) : make_float4(0.f, 0.f, 0.f, 0.f);
+          x[i][v] = in ? load4(static_cast<const T*>(f.v) + pr[i] * D + at[v]) : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        if (pr[i] < 0) continue;  // (the warp's)
+        float s = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPL; ++v)
+          s = fmaf(q[v].x, k[i][v].x, fmaf(q[v].y, k[i][v].y, fmaf(q[v].z, k[i][v].z, fmaf(q[v].w, k[i][v].w, s))));
+#pragma unroll
+        for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+        add(s, 1.f, x[i]);
+      }
+    }
+  }
+  for (int i = 0; i < own.n; ++i) {
+    const Place mine = own.at(p, y_row, i);
+    if (!mine.ml) continue;
+    const float2 ml = __ldcg(mine.ml);
+    float4 x[VPL];
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      x[v] = at[v] >= 0 ? __ldcg(reinterpret_cast<const float4*>(mine.rows + at[v])) : make_float4(0.f, 0.f, 0.f, 0.f);
+    add(ml.x, ml.y, x);
+  }
+  const float inv = L != 0.f ? 1.f / L : 0.f;
+  if (!y_in(p, y_row * D, D)) return;
+#pragma unroll
+  for (int v = 0; v < VPL; ++v)
+    if (at[v] >= 0) store4(static_cast<T*>(p.y) + y_row * D + at[v], a[v], inv);
+}
+
 // WPR warps take one (sequence, query head).  Its partials, in order: those of its
 // prefix (a whole unit's, or one of each slice that holds tiles of the unit), then those
 // of its own pages likewise.  A warp takes a run of them, 32 at a time: a lane each
@@ -221,7 +342,8 @@ struct JoinParams {
 // (64 sequences of 32 heads behind 8191 keys: 7 us, 26 with a CTA a row).
 constexpr int kJoinWarps = 8;
 
-template <typename T, int VPL, int WPR>
+// WINDOW: the call has one.
+template <typename T, int VPL, int WPR, bool WINDOW>
 __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __grid_constant__ JoinParams jp) {
   __shared__ float2 ml_s[kJoinWarps];
   __shared__ float4 acc_s[WPR > 1 ? kJoinWarps : 1][WPR > 1 ? VPL * 32 : 1];
@@ -260,6 +382,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __gr
   bool bad = n_own < 0 || n_own > static_cast<int64_t>(p.max_pages) * p.page_size;
   // the prefix' partials
   int n_pre = 0, s_pre = 0, r_pre = 0;
+  int first = 0, end = 0;  // the keys of the prefix that the row attends
   if (g >= 0 && g < f.G) {
     const int64_t b0 = pre_base(g);
     const Group gr = group_at(f, g);
@@ -273,33 +396,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __gr
       s_pre = parts.x;
       n_pre = parts.y;
       r_pre = r % f.rows;
+      first = first_key(f, gr.hi, n_own);
+      end = gr.hi;
     }
   }
-  // its own
-  int n_mine = 0, s_own = 0, slot_own = 0;
-  const int gr_own = hr / p.rows, r_own = hr - gr_own * p.rows;
-  if (const int64_t tiles = own1 - own0; tiles > 0) {
-    const Axis axis(p, own_total);
-    const int64_t u0 = own0 * p.units + static_cast<int64_t>(hk * p.groups + gr_own) * tiles;
-    s_own = axis.holds(u0);
-    n_mine = axis.holds(u0 + tiles - 1) - s_own + 1;
-    slot_own = axis.start(s_own) < u0 ? 1 : 0;
-  }
-  const int n = bad ? 0 : n_pre + n_mine;
-  // partial i: its (max, sum) and its row
-  struct Place {
-    const float2* ml;
-    const float* rows;
-  };
+  const OwnParts own(p, own0, own1, own_total, hk, hr);
+  const int n = bad ? 0 : n_pre + own.n;
   auto at = [&](int i) -> Place {
-    if (i < n_pre) {
-      if (n_pre == 1) return whole_in(f, row) ? Place{f.whole_ml + row, f.whole + row * D} : Place{nullptr, nullptr};
-      const int64_t x = (static_cast<int64_t>(s_pre + i) * 2 + (i == 0)) * f.rows + r_pre;
-      return slice_in(f, x, 1) ? Place{f.ml + x, f.part + x * D} : Place{nullptr, nullptr};
-    }
-    if (n_mine == 1) return own_in(p, row, 1) ? Place{p.own_ml + row, p.own_part + row * D} : Place{nullptr, nullptr};
-    const int64_t x = (static_cast<int64_t>(s_own + i - n_pre) * 2 + (i == n_pre ? slot_own : 0)) * p.rows + r_own;
-    return part_in(p, x, 1, static_cast<int64_t>(p.slices) * 2) ? Place{p.ml + x, p.part + x * D} : Place{nullptr, nullptr};
+    if (i >= n_pre) return own.at(p, row, i - n_pre);
+    if (n_pre == 1) return whole_in(f, row) ? Place{f.whole_ml + row, f.whole + row * D} : Place{nullptr, nullptr};
+    const int64_t x = (static_cast<int64_t>(s_pre + i) * 2 + (i == 0)) * f.rows + r_pre;
+    return slice_in(f, x, 1) ? Place{f.ml + x, f.part + x * D} : Place{nullptr, nullptr};
   };
 
   const int part = warp % WPR, i0 = n * part / WPR, i1 = n * (part + 1) / WPR;
@@ -386,6 +493,16 @@ __global__ void __launch_bounds__(kJoinWarps * 32) prefix_join_kernel(const __gr
       }
     }
   }
+  if (WINDOW && first > 0 && n > 0) {  // its window leaves keys out that others of its group may attend
+    bool odd = false;
+#pragma unroll
+    for (int v = 0; v < VPL; ++v)
+      odd |= !(fabsf(a[v].x) < INFINITY && fabsf(a[v].y) < INFINITY && fabsf(a[v].z) < INFINITY && fabsf(a[v].w) < INFINITY);
+    if (__any_sync(0xffffffffu, odd)) {
+      if constexpr (WINDOW) attend_alone<T, VPL>(jp, g, b, h, first, end, own);
+      return;
+    }
+  }
   const float inv = L != 0.f ? 1.f / L : 0.f;  // no key: a zero row
   const int64_t y_at = row * D;
   if (!y_in(p, y_at, D)) return;
@@ -401,8 +518,9 @@ cudaError_t launch_join_d(const JoinParams& jp, cudaStream_t s) {
   // a warp a row where that fills a good part of the GPU's warps, else a CTA a row
   const bool many = rows >= int64_t(num_sms()) * 4;
   PdlLaunch l(dim3(static_cast<unsigned>(many ? (rows + kJoinWarps - 1) / kJoinWarps : rows)), kJoinWarps * 32, 0, s);
-  cudaError_t e = many ? cudaLaunchKernelEx(&l.cfg, prefix_join_kernel<T, VPL, 1>, jp)
-                       : cudaLaunchKernelEx(&l.cfg, prefix_join_kernel<T, VPL, kJoinWarps>, jp);
+  auto go = [&](auto one, auto several) { return cudaLaunchKernelEx(&l.cfg, many ? one : several, jp); };
+  cudaError_t e = jp.pre.window > 0 ? go(prefix_join_kernel<T, VPL, 1, true>, prefix_join_kernel<T, VPL, kJoinWarps, true>)
+                                    : go(prefix_join_kernel<T, VPL, 1, false>, prefix_join_kernel<T, VPL, kJoinWarps, false>);
   return e != cudaSuccess ? e : cudaGetLastError();
 }
 

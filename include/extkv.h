@@ -552,9 +552,8 @@ size_t attention_paged_decode_fp8_workspace_size(int64_t B, int64_t Hq, int64_t 
  *     row, or those of the group's sequences, are zero rows.  A cu_groups that breaks its rules is flagged
  *     EXTKV_DEV_BAD_SEQLENS, and nothing is written.  Bad pages as in
  *     attention_paged_decode.
- *   - Slots outside the ranges never reach the result, whatever they hold.  A row of V in
- *     the prefix that some row of the group attends and that holds an infinity or a NaN may
- *     reach every row of the group, also those whose window leaves it out, as 0 * infinity does.
+ *   - Slots outside the ranges never reach the result, whatever they hold, nor do slots of a
+ *     prefix that a sequence's window leaves out, although others of its group attend them.
  *   - Statistics, sums and joins as attention_paged_decode; scale likewise.  D % 8 == 0,
  *     8 <= D <= 512.  bf16 with D in {64,128,256} and page_size a multiple of 16 attends the
  *     prefix on the tcgen05 tensor cores, every other shape on fp32 SIMT; the

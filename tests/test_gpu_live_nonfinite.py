@@ -1,6 +1,6 @@
 """Infinities and NaN in live slots: they reach the rows that attend them, in the columns where
-the definition has them, and no other row, head or column; but for a prefix' row of V, which in
-its columns may also reach rows of its group whose window leaves it out."""
+the definition has them, and no other head or column, nor any other sequence's rows (those of a
+prefix' group whose window leaves the slot out: test_gpu_window_isolation.py)."""
 import math
 
 import pytest
